@@ -98,10 +98,10 @@ def _ints(text):
 
 
 def _exponents(amax):
-    """The least e with amax <= 448 * 2^e (448 = 0.875 * 2^9), within [-118, 119]; 0 for a row of zeros."""
+    """The least e within [-118, 119] with amax <= 448 * 2^e (448 = 0.875 * 2^9)."""
     m, ex = torch.frexp(amax)
     e = torch.where(m <= 0.875, ex - 9, ex - 8).clamp(-118, 119)
-    return torch.where(amax == 0, torch.zeros_like(e), e)
+    return torch.where(amax == 0, torch.full_like(e, -118), e)
 
 
 def _rows_of(x, kv_type):
@@ -329,7 +329,7 @@ def exact(case, seed):
                 for _ in range(3):
                     power = power + (448 * torch.pow(2.0, power) < peak)
                 power = power.clamp(-118, 119)
-                x = torch.where(peak > 0, x / torch.pow(2.0, power), x)
+                x = torch.where(peak > 0, x / torch.pow(2.0, power), x)   # a row of zeros is zeros at any scale
             at = 0
             for b, (T, S) in enumerate(zip(s["q_len"], s["kv"])):
                 after.view(-1, after.shape[2])[slot_of(b, torch.arange(S - T, S, device=dev)), :w] = x[at:at + T].flatten(1)
