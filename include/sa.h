@@ -264,6 +264,111 @@ sa_status sa_sparse_attn_decode_rows(const void* q, const void* k_rows, const vo
                                      void* ws, size_t ws_bytes, sa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Paged K/V cache, in bf16 or in 8 bits (no counterpart in the pages, whose
+ * caches are contiguous: an extension for serving, where sequences grow and
+ * end, and for twice the positions per byte).
+ *
+ * A pool holds num_pages pages of page_size cache rows; K and V have a pool
+ * each, of the same shape.  A row is one position of one sequence, all kv
+ * heads, sa_paged_row_bytes(kv_type, Hkv) bytes:
+ *   SA_KV_BF16   Hkv * 128 bf16 values, then 16 zero bytes (the layout of
+ *                sa_gather_rows)
+ *   SA_KV_E4M3   Hkv * 128 OCP E4M3 codes, then one scale byte per kv head
+ *                (E8M0: 2^(byte - 127), 255 is NaN), then zeros to 16 bytes;
+ *                value = code * 2^(byte - 127)
+ * block_table [B, max_pages] int32: position j of sequence b is row
+ * j % page_size of page block_table[b, j / page_size].  Entries for positions
+ * no call reaches are not read.  A used page outside [0, num_pages) is a
+ * caller error: reads take a page within the pool instead (never faulting),
+ * a write of that row is dropped.
+ *
+ * New tokens of all sequences are packed: sequence b owns tokens
+ * q_start[b] .. q_start[b + 1] - 1 (q_start [B + 1] int32, ascending, clamped
+ * to [0, N] on the device), which are the LAST q_len = q_start[b + 1] -
+ * q_start[b] of its kv_len[b] positions (kv_len [B] int32, clamped to
+ * [0, max_pages * page_size]): token t sits at position kv_len[b] - q_len + t.
+ * A sequence may have no new token.  Tokens before q_start[0] or from
+ * q_start[B] on belong to no sequence: nothing is read or written for them.
+ *
+ * Supported: D = 128; 1 <= Hkv <= 8; page_size a power of two from 16 to 256;
+ * num_pages * page_size and max_pages * page_size below 2^31.  Pools are
+ * 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+typedef enum { SA_KV_BF16 = 0, SA_KV_E4M3 = 1 } sa_kv_type;
+#define SA_PAGED_MAX_HKV 8
+
+/* Bytes of a cache row (0 for a bad type or Hkv). */
+size_t sa_paged_row_bytes(int kv_type, int Hkv);
+
+/* Writes the new tokens' K and V into their rows, padding included.  E4M3:
+ * the scale of a token and kv head is 2^e, e the least integer in [-118, 119]
+ * with max |x| <= 448 * 2^e over its 128 finite values (-118 for zeros); a
+ * code is x / 2^e rounded to nearest even, magnitudes above 448 (only at
+ * e = 119) clamped; infinities and NaN become the NaN code.  Every value so
+ * stored is exact in bf16.
+ *   k_new, v_new  [N, Hkv, 128] bf16, 16-byte aligned; tokens k_stride and
+ *                 v_stride elements apart (multiples of 8, >= Hkv * 128), so
+ *                 slices of a fused projection are taken as they are
+ * A token whose position is negative (kv_len[b] < q_len) or beyond the table
+ * is dropped.  Two tokens of one call must not share a row (the row is then
+ * that of neither).  All other bytes of the pools stay as they are. */
+sa_status sa_paged_kv_write(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                            const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                            int B, int N, int max_pages, int num_pages, int page_size, int Hkv, int D,
+                            int kv_type, void* k_pages, void* v_pages, sa_stream_t stream);
+
+/* Reads selected rows back: k_rows, v_rows [B, k, Hkv * D + 8] bf16, the
+ * compact rows of sa_gather_rows (for sa_sparse_attn_decode_rows), values
+ * rounded to bf16 (exact for rows that sa_paged_kv_write wrote); zeros for
+ * rows from count[b] on and in the pad.
+ *   idx [B, k] int32 positions (used ones outside [0, max_pages * page_size)
+ *   are clamped); count [B] int32 (clamped to [0, k]); the row buffers are
+ *   16-byte aligned.  1 <= k <= 2^20. */
+sa_status sa_paged_kv_gather(const void* k_pages, const void* v_pages, const int32_t* block_table,
+                             const int32_t* idx, const int32_t* count, int B, int max_pages, int num_pages,
+                             int page_size, int Hkv, int D, int k, int kv_type, void* k_rows, void* v_rows,
+                             sa_stream_t stream);
+
+/* Attention of a chunk of new tokens over the paged cache: token t of
+ * sequence b, query head h (kv head g = h / (Hq / Hkv)), at position p:
+ *   z_j = scale * q . k_j, j = 0 .. p;  out = sum_j softmax(z)_j v_j
+ *   lse = ln sum_j exp(z_j)
+ * The chunk's own K and V are read from the cache too: write them first.
+ * A token with p < 0 attends to nothing: out 0, lse -inf.  scale <= 0
+ * selects 1/sqrt(D).  What rows beyond p hold, infinities and NaN included,
+ * has no effect.  fp32 accumulation and softmax, bf16 output.
+ *   q     [N, Hq, 128] bf16, 16-byte aligned, tokens q_stride elements apart
+ *         (a multiple of 8, >= Hq * 128)
+ *   max_q an upper bound of every q_len (1 for decode); tokens from max_q on
+ *         of a sequence are not computed
+ *   out   [N, Hq, 128] bf16, contiguous; lse [N, Hq] fp32 or NULL; rows of
+ *         tokens that belong to no sequence are left as they were
+ *   ws    >= sa_paged_attn_workspace(...) bytes (zero-filled before first
+ *         use; see the conventions above).  Its first int32 is the kernel
+ *         error word: 0 after a good call, else the outputs hold NaN.
+ * Supported: Hq % Hkv == 0; Hq/Hkv <= 16; N * Hq < 2^31. */
+size_t sa_paged_attn_workspace(int B, int N, int max_q, int Hq, int Hkv, int D, int kv_type);
+sa_status sa_paged_attn(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                        const int32_t* block_table, const int32_t* q_start, const int32_t* kv_len, int B, int N,
+                        int max_q, int max_pages, int num_pages, int page_size, int Hq, int Hkv, int D,
+                        int kv_type, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                        sa_stream_t stream);
+
+/* sa_sparse_attn_decode over the paged cache: one query token per sequence,
+ * attending to the positions idx[b, 0 .. count[b]).
+ *   q [B, Hq, 128] bf16, 16-byte aligned, contiguous; idx [B, k] int32 (used
+ *   ones outside [0, max_pages * page_size) are clamped); count [B] int32
+ *   (clamped to [0, k]); out [B, Hq, 128] bf16; lse [B, Hq] fp32 or NULL
+ *   ws >= sa_paged_sparse_attn_decode_workspace(...) bytes, as above.
+ * Supported: as for sa_paged_attn; 1 <= k <= 2^20. */
+size_t sa_paged_sparse_attn_decode_workspace(int B, int Hq, int Hkv, int D, int k, int kv_type);
+sa_status sa_paged_sparse_attn_decode(const void* q, const void* k_pages, const void* v_pages,
+                                      const int32_t* block_table, const int32_t* idx, const int32_t* count, int B,
+                                      int max_pages, int num_pages, int page_size, int Hq, int Hkv, int D, int k,
+                                      int kv_type, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                                      sa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Decode attention without a caller workspace.
  *
  * No counterpart in the paper: this is an interface for callers that cannot
@@ -403,8 +508,8 @@ sa_status sa_index_pattern_greedy(const double* overlap, int n_layers, int n_ful
  *
  * Waits for the work queued on `stream` so far (synchronizes it), then reads
  * the kernel error word at the start of `ws`, the workspace of any call above
- * that takes one (indexer top-k of every form, gist routing, decode
- * attention).  Returns SA_OK when the word is zero and SA_ERR_TIMEOUT when a
+ * that takes one (indexer top-k of every form, gist routing, decode and
+ * paged attention).  Returns SA_OK when the word is zero and SA_ERR_TIMEOUT when a
  * pipeline wait of a call that used the workspace gave up; sa_last_error()
  * then names the wait's code.  The word is left as it is (zero-fill the
  * workspace to use it again).  SA_ERR_INVALID_ARG for a NULL ws,
@@ -425,10 +530,12 @@ sa_status sa_workspace_status(const void* ws, sa_stream_t stream);
  *   sa_debug_enabled(): 1 in a debug build, 0 otherwise.
  *   sa_debug_read(record, reset): host int32[4] = {code of the first
  *     violation (0 none, 1 prefill attention index, 2 decode attention index,
- *     3 gathered-rows index, 4 workspace canary), its first detail (the index;
- *     for a canary the call: 1 index top-k, 2 multi-head top-k, 3 decode
- *     attention, 4 gist routing, 5 fp8 top-k), its second detail (Tk_max; for a canary the
- *     first changed byte), number of violations}; reset != 0 clears it.
+ *     3 gathered-rows index, 4 workspace canary, 5 page of a block table,
+ *     6 position of a paged call), its first detail (the index; for a canary
+ *     the call: 1 index top-k, 2 multi-head top-k, 3 decode attention, 4 gist
+ *     routing, 5 fp8 top-k, 6 paged attention), its second detail (the bound
+ *     it is outside of; for a canary the first changed byte), number of
+ *     violations}; reset != 0 clears it.
  *     Synchronous; the release build reports zeros.
  * ---------------------------------------------------------------------- */
 int sa_debug_enabled(void);

@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "../../include/sa.h"
+#include "paged.cuh"
 #include "sa_common.cuh"
 #include "sa_internal.h"
 
@@ -91,6 +92,35 @@ sa_status validate_attn(const void* q, const void* kc, const void* vc, const int
     return fail(SA_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
   if (!aligned(idx, 4) || !aligned(count, 4)) return fail(SA_ERR_INVALID_ARG, "idx/count misaligned");
   return SA_OK;
+}
+
+// Sizes of a paged cache and its block table.
+sa_status validate_paged(int B, int max_pages, int num_pages, int page_size, int Hkv, int D, int kv_type) {
+  if (B < 0 || max_pages < 1 || num_pages < 1 || Hkv < 1)
+    return fail(SA_ERR_INVALID_ARG, "bad sizes: B=%d max_pages=%d num_pages=%d Hkv=%d", B, max_pages, num_pages, Hkv);
+  if (kv_type != SA_KV_BF16 && kv_type != SA_KV_E4M3) return fail(SA_ERR_INVALID_ARG, "bad kv_type %d", kv_type);
+  if (D != SA_HEAD_DIM) return fail(SA_ERR_UNSUPPORTED, "D=%d unsupported (only %d)", D, SA_HEAD_DIM);
+  if (Hkv > SA_PAGED_MAX_HKV)
+    return fail(SA_ERR_UNSUPPORTED, "Hkv=%d > %d unsupported for paged caches", Hkv, SA_PAGED_MAX_HKV);
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0)
+    return fail(SA_ERR_UNSUPPORTED, "page_size=%d unsupported (a power of two from 16 to 256)", page_size);
+  if ((long long)num_pages * page_size > 0x7FFFFFFFll || (long long)max_pages * page_size > 0x7FFFFFFFll)
+    return fail(SA_ERR_UNSUPPORTED, "num_pages=%d or max_pages=%d too large: rows are numbered in 31 bits", num_pages,
+                max_pages);
+  return SA_OK;
+}
+
+sa_status validate_paged_heads(int Hq, int Hkv) {
+  if (Hq < 1) return fail(SA_ERR_INVALID_ARG, "Hq=%d must be >= 1", Hq);
+  if (Hq % Hkv != 0) return fail(SA_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
+  if (Hq / Hkv > 16) return fail(SA_ERR_UNSUPPORTED, "Hq/Hkv=%d > 16 unsupported", Hq / Hkv);
+  return SA_OK;
+}
+
+int page_shift_of(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
 }
 
 }  // namespace
@@ -478,6 +508,173 @@ sa_status sa_sparse_attn_decode_rows(const void* q, const void* k_rows, const vo
   if (e != cudaSuccess) return cuda_fail(e, "attn_decode_rows launch");
   if ((e = sa::dbg_check(ws, need - sa::kWsCanary, 3, as_cuda(stream))) != cudaSuccess)
     return cuda_fail(e, "debug canary");
+  return ok();
+}
+
+// ----------------------------------------------------------- paged cache
+
+size_t sa_paged_row_bytes(int kv_type, int Hkv) {
+  if ((kv_type != SA_KV_BF16 && kv_type != SA_KV_E4M3) || Hkv < 1 || Hkv > SA_PAGED_MAX_HKV) return 0;
+  return (size_t)sa::paged_row_bytes(kv_type == SA_KV_E4M3, Hkv);
+}
+
+sa_status sa_paged_kv_write(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                            const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, int B, int N,
+                            int max_pages, int num_pages, int page_size, int Hkv, int D, int kv_type, void* k_pages,
+                            void* v_pages, sa_stream_t stream) {
+  sa_status st = validate_paged(B, max_pages, num_pages, page_size, Hkv, D, kv_type);
+  if (st != SA_OK) return st;
+  if (N < 0) return fail(SA_ERR_INVALID_ARG, "N=%d must be >= 0", N);
+  if (N > (1 << 30)) return fail(SA_ERR_UNSUPPORTED, "N=%d too large", N);
+  if (B == 0 || N == 0) return ok();
+  if (!k_new || !v_new || !q_start || !kv_len || !block_table || !k_pages || !v_pages)
+    return fail(SA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16))
+    return fail(SA_ERR_INVALID_ARG, "k_new, v_new and the pools must be 16-byte aligned");
+  if (k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return fail(SA_ERR_INVALID_ARG, "token strides must be multiples of 8 elements and at least Hkv*D");
+  if (!aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4))
+    return fail(SA_ERR_INVALID_ARG, "q_start/kv_len/block_table misaligned");
+  int* rec = nullptr;
+  cudaError_t e = sa::dbg_record(&rec);
+  if (e != cudaSuccess) return cuda_fail(e, "debug record");
+  e = sa::launch_paged_write(static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new), k_stride,
+                             v_stride, q_start, kv_len, block_table, B, N, max_pages, num_pages,
+                             page_shift_of(page_size), Hkv, kv_type == SA_KV_E4M3, static_cast<uint8_t*>(k_pages),
+                             static_cast<uint8_t*>(v_pages), rec, as_cuda(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_write launch");
+  return ok();
+}
+
+sa_status sa_paged_kv_gather(const void* k_pages, const void* v_pages, const int32_t* block_table, const int32_t* idx,
+                             const int32_t* count, int B, int max_pages, int num_pages, int page_size, int Hkv, int D,
+                             int k, int kv_type, void* k_rows, void* v_rows, sa_stream_t stream) {
+  sa_status st = validate_paged(B, max_pages, num_pages, page_size, Hkv, D, kv_type);
+  if (st != SA_OK) return st;
+  if (k < 1) return fail(SA_ERR_INVALID_ARG, "k=%d must be >= 1", k);
+  if (k > (1 << 20)) return fail(SA_ERR_UNSUPPORTED, "k=%d too large", k);
+  if (B > 65535) return fail(SA_ERR_UNSUPPORTED, "B=%d too large", B);
+  if (B == 0) return ok();
+  if (!k_pages || !v_pages || !block_table || !idx || !count || !k_rows || !v_rows)
+    return fail(SA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_rows, 16) || !aligned(v_rows, 16))
+    return fail(SA_ERR_INVALID_ARG, "pools and row buffers must be 16-byte aligned");
+  if (!aligned(idx, 4) || !aligned(count, 4) || !aligned(block_table, 4))
+    return fail(SA_ERR_INVALID_ARG, "idx/count/block_table misaligned");
+  int* rec = nullptr;
+  cudaError_t e = sa::dbg_record(&rec);
+  if (e != cudaSuccess) return cuda_fail(e, "debug record");
+  e = sa::launch_paged_gather(static_cast<const uint8_t*>(k_pages), static_cast<const uint8_t*>(v_pages), block_table,
+                              idx, count, B, max_pages, num_pages, page_shift_of(page_size), Hkv, k,
+                              kv_type == SA_KV_E4M3, static_cast<uint16_t*>(k_rows), static_cast<uint16_t*>(v_rows),
+                              rec, as_cuda(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_gather launch");
+  return ok();
+}
+
+size_t sa_paged_attn_workspace(int B, int N, int max_q, int Hq, int Hkv, int D, int kv_type) {
+  (void)D;
+  if (B <= 0 || N <= 0 || max_q <= 0 || Hkv <= 0 || Hkv > SA_PAGED_MAX_HKV || Hq < Hkv || Hq % Hkv != 0 ||
+      Hq / Hkv > 16)
+    return 0;
+  return sa::paged_attn_workspace_bytes(kv_type == SA_KV_E4M3, B, N, max_q < N ? max_q : N, Hkv, Hq / Hkv) +
+         sa::kWsCanary;
+}
+
+sa_status sa_paged_attn(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                        const int32_t* block_table, const int32_t* q_start, const int32_t* kv_len, int B, int N,
+                        int max_q, int max_pages, int num_pages, int page_size, int Hq, int Hkv, int D, int kv_type,
+                        float scale, void* out, float* lse, void* ws, size_t ws_bytes, sa_stream_t stream) {
+  sa_status st = validate_paged(B, max_pages, num_pages, page_size, Hkv, D, kv_type);
+  if (st != SA_OK) return st;
+  if ((st = validate_paged_heads(Hq, Hkv)) != SA_OK) return st;
+  if (N < 0 || max_q < 0) return fail(SA_ERR_INVALID_ARG, "bad sizes: N=%d max_q=%d", N, max_q);
+  if ((long long)N * Hq > 0x7FFFFFFFll) return fail(SA_ERR_UNSUPPORTED, "N*Hq=%lld too large", (long long)N * Hq);
+  if (B == 0 || N == 0 || max_q == 0) return ok();
+  if (!q || !k_pages || !v_pages || !block_table || !q_start || !kv_len || !out)
+    return fail(SA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16))
+    return fail(SA_ERR_INVALID_ARG, "q, the pools and out must be 16-byte aligned");
+  if (q_stride < (int64_t)Hq * D || q_stride % 8 != 0)
+    return fail(SA_ERR_INVALID_ARG, "q_stride must be a multiple of 8 elements and at least Hq*D");
+  if (!aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4) || (lse && !aligned(lse, 4)))
+    return fail(SA_ERR_INVALID_ARG, "q_start/kv_len/block_table/lse misaligned");
+  if (max_q > N) max_q = N;
+  if ((long long)B * max_q > (1ll << 30))
+    return fail(SA_ERR_UNSUPPORTED, "B*max_q=%lld too large", (long long)B * max_q);
+  const size_t need = sa_paged_attn_workspace(B, N, max_q, Hq, Hkv, D, kv_type);
+  if ((st = check_ws(ws, ws_bytes, need)) != SA_OK) return st;
+  sa::PagedArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.kp = static_cast<const uint8_t*>(k_pages);
+  a.vp = static_cast<const uint8_t*>(v_pages);
+  a.table = block_table;
+  a.B = B, a.N = N, a.max_q = max_q, a.max_pages = max_pages, a.num_pages = num_pages;
+  a.page_shift = page_shift_of(page_size);
+  a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv;
+  a.qscale = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * sa::kPgLog2e;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  cudaStream_t cs = as_cuda(stream);
+  cudaError_t e = sa::dbg_record(&a.dbg);
+  if (e != cudaSuccess) return cuda_fail(e, "debug record");
+  if ((e = sa::dbg_arm(ws, need - sa::kWsCanary, cs)) != cudaSuccess) return cuda_fail(e, "debug canary");
+  if ((e = sa::launch_paged_attn(a, kv_type == SA_KV_E4M3, ws, cs)) != cudaSuccess)
+    return cuda_fail(e, "paged_attn launch");
+  if ((e = sa::dbg_check(ws, need - sa::kWsCanary, 6, cs)) != cudaSuccess) return cuda_fail(e, "debug canary");
+  return ok();
+}
+
+size_t sa_paged_sparse_attn_decode_workspace(int B, int Hq, int Hkv, int D, int k, int kv_type) {
+  (void)D;
+  if (B <= 0 || k <= 0 || Hkv <= 0 || Hkv > SA_PAGED_MAX_HKV || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 16) return 0;
+  return sa::paged_rows_workspace_bytes(kv_type == SA_KV_E4M3, B, Hkv, Hq / Hkv, 1) + sa::kWsCanary;
+}
+
+sa_status sa_paged_sparse_attn_decode(const void* q, const void* k_pages, const void* v_pages,
+                                      const int32_t* block_table, const int32_t* idx, const int32_t* count, int B,
+                                      int max_pages, int num_pages, int page_size, int Hq, int Hkv, int D, int k,
+                                      int kv_type, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                                      sa_stream_t stream) {
+  sa_status st = validate_paged(B, max_pages, num_pages, page_size, Hkv, D, kv_type);
+  if (st != SA_OK) return st;
+  if ((st = validate_paged_heads(Hq, Hkv)) != SA_OK) return st;
+  if (k < 1) return fail(SA_ERR_INVALID_ARG, "k=%d must be >= 1", k);
+  if (k > (1 << 20)) return fail(SA_ERR_UNSUPPORTED, "k=%d too large", k);
+  if ((long long)B * Hq > (1ll << 30)) return fail(SA_ERR_UNSUPPORTED, "B*Hq=%lld too large", (long long)B * Hq);
+  if (B == 0) return ok();
+  if (!q || !k_pages || !v_pages || !block_table || !idx || !count || !out)
+    return fail(SA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16))
+    return fail(SA_ERR_INVALID_ARG, "q, the pools and out must be 16-byte aligned");
+  if (!aligned(idx, 4) || !aligned(count, 4) || !aligned(block_table, 4) || (lse && !aligned(lse, 4)))
+    return fail(SA_ERR_INVALID_ARG, "idx/count/block_table/lse misaligned");
+  const size_t need = sa_paged_sparse_attn_decode_workspace(B, Hq, Hkv, D, k, kv_type);
+  if ((st = check_ws(ws, ws_bytes, need)) != SA_OK) return st;
+  sa::PagedArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = (long long)Hq * D;
+  a.idx = idx;
+  a.count = count;
+  a.kp = static_cast<const uint8_t*>(k_pages);
+  a.vp = static_cast<const uint8_t*>(v_pages);
+  a.table = block_table;
+  a.B = B, a.N = B, a.max_q = 1, a.max_pages = max_pages, a.num_pages = num_pages;
+  a.page_shift = page_shift_of(page_size);
+  a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv, a.k = k;
+  a.qscale = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * sa::kPgLog2e;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  cudaStream_t cs = as_cuda(stream);
+  cudaError_t e = sa::dbg_record(&a.dbg);
+  if (e != cudaSuccess) return cuda_fail(e, "debug record");
+  if ((e = sa::dbg_arm(ws, need - sa::kWsCanary, cs)) != cudaSuccess) return cuda_fail(e, "debug canary");
+  if ((e = sa::launch_paged_rows(a, kv_type == SA_KV_E4M3, ws, cs)) != cudaSuccess)
+    return cuda_fail(e, "paged_sparse_attn_decode launch");
+  if ((e = sa::dbg_check(ws, need - sa::kWsCanary, 6, cs)) != cudaSuccess) return cuda_fail(e, "debug canary");
   return ok();
 }
 

@@ -1,0 +1,994 @@
+// Paged K/V cache (sm_100a): writing new rows (E4M3 quantisation or a copy),
+// reading selected rows back, and attention with few query rows per kv head
+// over the pages -- one token per sequence over selected rows, or a short
+// chunk of tokens over every row up to its own.
+//
+// Rows and scales: see paged.cuh.  The scale of one position and kv head is a
+// power of two, 2^e with e the least integer such that max|x| <= 448 * 2^e:
+// E4M3 has the same relative step at every magnitude, so a finer scale would
+// gain no precision, and a power of two makes x * 2^-e, code * 2^e and the
+// value's bf16 form exact; the rounding to a code is the only one.
+//
+// Few-row attention: softmax(scale q.K^T) V by one pass with a running
+// maximum and sum.  It reads the cache once, 2 * row bytes per position for
+// 4 * 128 * Hq flops, so it is bound by HBM; the row side of the matrix
+// instructions (mma.sync, 16 rows) holds the G query heads of the chunk's
+// tokens, which share the kv head's rows.
+//
+//   paged_write_kernel       one warp per (token, K or V)
+//   paged_gather_kernel      one warp per selected row (K and V)
+//   paged_attn_rows_kernel   units of (16-row block of queries, tile of
+//       positions, all kv heads), flattened over the batch and cut evenly
+//       over one CTA per SM; partials of (max, sum, output)
+//   paged_attn_rows_merge_kernel   folds them by the log-sum-exp rule
+#include "paged.cuh"
+#include "tc_common.cuh"
+
+namespace sa {
+namespace {
+
+// ------------------------------------------------------------------- write
+
+// One new row x (Hkv * 128 bf16) -> a cache row.  Half a warp holds one head:
+// lane j of the half 8 values (16 bytes).
+template <bool FP8>
+__device__ __forceinline__ void write_row(const uint16_t* __restrict__ x, uint8_t* __restrict__ row, int Hkv) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, j = lane & 15;
+  uint4 v[4];
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int h = 2 * it + half;
+    v[it] = h < Hkv ? __ldg(reinterpret_cast<const uint4*>(x + h * kPgD) + j) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  if constexpr (!FP8) {
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int h = 2 * it + half;
+      if (h < Hkv) reinterpret_cast<uint4*>(row + h * (2 * kPgD))[j] = v[it];
+    }
+    if (lane == 0) *reinterpret_cast<uint4*>(row + Hkv * (2 * kPgD)) = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    uint32_t tail[2] = {0u, 0u};   // the scale bytes of heads 0-3 and 4-7
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+      // largest finite magnitude: bf16 magnitudes compare as integers
+      uint32_t am = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+        am = max(am, lo < 0x7f80u ? lo : 0u);
+        am = max(am, hi < 0x7f80u ? hi : 0u);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+      // am = 2^(E - 127) * (1 + M / 128); 448 = 2^8 * 1.75, so the least e
+      // with am <= 448 * 2^e is E - 135, or E - 134 when 1 + M / 128 > 1.75
+      const int E = (int)(am >> 7), M = (int)(am & 0x7fu);
+      int e = E - (M > 0x60 ? 134 : 135);
+      e = min(max(e, -118), 119);   // 448 * 2^119 and 2^-9 * 2^-118 are bf16 values
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+      uint32_t c[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo = bf_lo(w[i]), hi = bf_hi(w[i]);
+        lo = isinf(lo) ? __uint_as_float(0x7fc00000u) : lo * inv;   // E4M3 has no infinity
+        hi = isinf(hi) ? __uint_as_float(0x7fc00000u) : hi * inv;
+        uint16_t r;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+        if (i & 1) c[i >> 1] |= (uint32_t)r << 16;
+        else c[i >> 1] = r;
+      }
+      const int h = 2 * it + half;
+      if (h < Hkv) reinterpret_cast<uint2*>(row + h * kPgD)[j] = make_uint2(c[0], c[1]);
+      const uint32_t b0 = (uint32_t)__shfl_sync(0xffffffffu, e, 0) + 127u;
+      const uint32_t b1 = (uint32_t)__shfl_sync(0xffffffffu, e, 16) + 127u;
+      if (2 * it < Hkv) tail[it >> 1] |= b0 << (16 * (it & 1));
+      if (2 * it + 1 < Hkv) tail[it >> 1] |= b1 << (16 * (it & 1) + 8);
+    }
+    if (lane == 0) *reinterpret_cast<uint4*>(row + Hkv * kPgD) = make_uint4(tail[0], tail[1], 0u, 0u);
+  }
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(256)
+paged_write_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new, long long k_stride,
+                   long long v_stride, const int32_t* __restrict__ q_start, const int32_t* __restrict__ kv_len,
+                   const int32_t* __restrict__ table, int B, int N, int max_pages, int num_pages, int page_shift,
+                   int Hkv, uint8_t* __restrict__ kp, uint8_t* __restrict__ vp, int* dbg) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int i = w >> 1;   // token; even warps K, odd warps V
+  if (i >= N) return;
+  const int b = seq_of_token(q_start, B, i);
+  if (b < 0) return;      // in front of the first sequence or behind the last
+  const int capacity = max_pages << page_shift;
+  const SeqSpan s = seq_span(q_start, kv_len, b, N, capacity);
+  const int pos = s.pos0 + (i - s.begin);
+  if (pos < 0) return;    // kv_len does not count this token: it has no place
+  const int pg = table[(long long)b * max_pages + (pos >> page_shift)];
+  if (pg < 0 || pg >= num_pages) {   // no page: the token is dropped, no other page is touched
+    if ((threadIdx.x & 31) == 0) paged_note(dbg, kDbgPage, pg, num_pages);
+    return;
+  }
+  const long long slot = ((long long)pg << page_shift) + (pos & ((1 << page_shift) - 1));
+  const long long off = slot * paged_row_bytes(FP8, Hkv);
+  if (w & 1) write_row<FP8>(v_new + (long long)i * v_stride, vp + off, Hkv);
+  else write_row<FP8>(k_new + (long long)i * k_stride, kp + off, Hkv);
+}
+
+// ------------------------------------------------------------------ gather
+
+// One cache row -> a compact bf16 row (Hkv * 128 values, 8 zeros).
+template <bool FP8>
+__device__ __forceinline__ void read_row(const uint8_t* __restrict__ row, uint16_t* __restrict__ dst, int Hkv) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (!FP8) {
+    for (int c = lane; c < Hkv * 16; c += 32)
+      reinterpret_cast<uint4*>(dst)[c] = __ldg(reinterpret_cast<const uint4*>(row) + c);
+  } else {
+    const uint2 tail = __ldg(reinterpret_cast<const uint2*>(row + Hkv * kPgD));
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {   // 8 lanes per head, 16 codes per lane
+      const int h = 4 * it + (lane >> 3), j = lane & 7;
+      if (h >= Hkv) break;
+      const uint4 c = __ldg(reinterpret_cast<const uint4*>(row + h * kPgD) + j);
+      const float s = e8m0_value(((it ? tail.y : tail.x) >> (8 * (h & 3))) & 0xffu);
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      uint32_t r[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[2 * i] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[i] & 0xffffu), s);
+        r[2 * i + 1] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[i] >> 16), s);
+      }
+      uint4* d = reinterpret_cast<uint4*>(dst + h * kPgD + j * 16);
+      d[0] = make_uint4(r[0], r[1], r[2], r[3]);
+      d[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+  }
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(256)
+paged_gather_kernel(const uint8_t* __restrict__ kp, const uint8_t* __restrict__ vp, const int32_t* __restrict__ table,
+                    const int32_t* __restrict__ idx, const int32_t* __restrict__ count, int max_pages, int num_pages,
+                    int page_shift, int Hkv, int k, uint16_t* __restrict__ ko, uint16_t* __restrict__ vo, int* dbg) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.y;
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= k) return;
+  const int c = count[b];
+  uint16_t* dk = ko + ((long long)b * k + r) * (Hkv * kPgD + 8);
+  uint16_t* dv = vo + ((long long)b * k + r) * (Hkv * kPgD + 8);
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  if (lane == 0) {
+    reinterpret_cast<uint4*>(dk)[Hkv * 16] = zero;
+    reinterpret_cast<uint4*>(dv)[Hkv * 16] = zero;
+  }
+  if (r >= c) {
+    for (int e = lane; e < Hkv * 16; e += 32) {
+      reinterpret_cast<uint4*>(dk)[e] = zero;
+      reinterpret_cast<uint4*>(dv)[e] = zero;
+    }
+    return;
+  }
+  const int capacity = max_pages << page_shift;
+  int j = idx[(long long)b * k + r];
+  if (j < 0 || j >= capacity) {
+    paged_note(dbg, kDbgPagedIndex, j, capacity);
+    j = j < 0 ? 0 : capacity - 1;
+  }
+  const int pg = checked_page(table[(long long)b * max_pages + (j >> page_shift)], num_pages, dbg);
+  const long long off =
+      (((long long)pg << page_shift) + (j & ((1 << page_shift) - 1))) * paged_row_bytes(FP8, Hkv);
+  read_row<FP8>(kp + off, dk, Hkv);
+  read_row<FP8>(vp + off, dv, Hkv);
+}
+
+// ------------------------------------------------------- few-row attention
+
+constexpr int kRwConsumers = 8;
+constexpr int kRwThreads = (kRwConsumers + 1) * 32;
+constexpr int kRwMaxStages = 8;
+constexpr int kRwBarBytes = 256;       // mbarriers, abort word, plan
+constexpr int kRwStageBytes = 208 * 1024;
+constexpr int kRwMergeThreads = 256;
+constexpr int kRwMergeMaxC = 1280;     // contributors of one (row block, head)
+
+struct RowsPlan {
+  int nrb, tb, RB;         // row blocks per sequence, tokens and rows of one
+  int P;                   // items: B * nrb
+  int wph, R;              // consumer warps per kv head, positions per tile
+  int row_bytes, stages;
+  int W;                   // CTAs
+};
+
+// Tiles of item p: the positions its last token attends to, or the selected
+// rows of its sequence.
+template <bool SPARSE>
+__device__ __forceinline__ int item_keys(const PagedArgs& a, const RowsPlan& pl, int p) {
+  if constexpr (SPARSE) {
+    return min(max(a.count[p], 0), a.k);
+  } else {
+    const int b = p / pl.nrb, t0 = p % pl.nrb * pl.tb;
+    const SeqSpan s = seq_span(a.q_start, a.kv_len, b, a.N, a.max_pages << a.page_shift);
+    const int n = min(s.len, a.max_q);
+    if (t0 >= n) return 0;
+    return max(s.pos0 + min(t0 + pl.tb, n), 0);
+  }
+}
+template <bool SPARSE>
+__device__ __forceinline__ int item_tiles(const PagedArgs& a, const RowsPlan& pl, int p) {
+  return (item_keys<SPARSE>(a, pl, p) + pl.R - 1) / pl.R;
+}
+
+// Sum over the block of v (threads kThreads, a multiple of 32), and the sum
+// over the threads before this one.  Every thread calls it.
+template <int kThreads>
+__device__ __forceinline__ long long block_scan(int v, long long& before, long long* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  long long base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) base += sh[w];
+    total += sh[w];
+  }
+  before = base + x - v;
+  return total;
+}
+
+// Query fragments (the M side): row r of the block is token t0 + r / G, head
+// r % G of kv head g.  For bf16 keys the usual layout; for codes, fp16 with
+// the reduction index permuted to what one ldmatrix of 16 codes gives (lane t
+// holds elements 4t .. 4t+3 of every 16), each row scaled by a power of two
+// that brings its largest magnitude to [2^14, 2^15): exact for every element
+// within 2^-31 of the largest, and undone in fp32 (`rowc`).
+template <bool FP8>
+__device__ __forceinline__ void load_q_rows(uint32_t (&qa)[8][4], float (&rowc)[2], const PagedArgs& a, int tok0,
+                                            int ntok, int g, bool active) {
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tg = lane & 3;
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    const int r = gq + 8 * hh;
+    const bool on = active && r < ntok * a.G;
+    const uint16_t* src = a.q + (long long)(tok0 + (on ? r / a.G : 0)) * a.q_stride +
+                          ((active ? g : 0) * a.G + (on ? r % a.G : 0)) * kPgD;
+    rowc[hh] = a.qscale;
+    if constexpr (!FP8) {
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        qa[kk][hh] = on ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * tg)) : 0u;
+        qa[kk][2 + hh] = on ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + 2 * tg)) : 0u;
+      }
+    } else {
+      uint2 v[8];
+      uint32_t am = 0u;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        v[kk] = on ? __ldg(reinterpret_cast<const uint2*>(src + kk * 16 + 4 * tg)) : make_uint2(0u, 0u);
+        const uint32_t w[2] = {v[kk].x, v[kk].y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+          am = max(am, lo < 0x7f80u ? lo : 0u);
+          am = max(am, hi < 0x7f80u ? hi : 0u);
+        }
+      }
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      const int e = min(max((int)(am >> 7) - 141, -100), 113);   // largest * 2^-e in [2^14, 2^15)
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+      rowc[hh] = a.qscale * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        qa[kk][hh] = pack_f16x2(bf_lo(v[kk].x) * inv, bf_hi(v[kk].x) * inv);
+        qa[kk][2 + hh] = pack_f16x2(bf_lo(v[kk].y) * inv, bf_hi(v[kk].y) * inv);
+      }
+    }
+  }
+}
+
+// D = A(16x16, row) * B(16x8, col) + D, fp16 inputs
+__device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Running state of one warp's 16 rows: output, its reference (base-2
+// logarithm), softmax maximum and sum.  For codes the output's reference mo
+// bounds z + log2(scale of v), so the weights that multiply the codes stay
+// within fp16; for bf16 it is the maximum itself.
+struct RowState {
+  float o[16][4];
+  float m[2], l[2], mo[2];
+};
+
+__device__ __forceinline__ void state_init(RowState& st) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) st.o[i][e] = 0.f;
+  st.m[0] = st.m[1] = st.mo[0] = st.mo[1] = -INFINITY;
+  st.l[0] = st.l[1] = 0.f;
+}
+
+// Zeroes the halves of a pair of 16-bit values whose bit in `keep` is clear.
+__device__ __forceinline__ uint32_t keep_halves(uint32_t v, bool lo, bool hi) {
+  return v & ((lo ? 0x0000ffffu : 0u) | (hi ? 0xffff0000u : 0u));
+}
+// Whether either half is infinite or NaN (exponent bits `ex` all ones).
+__device__ __forceinline__ uint32_t clean_halves(uint32_t v, uint32_t ex, bool& bad) {
+  const bool lo = (v & ex) == ex, hi = ((v >> 16) & ex) == ex;
+  bad |= lo || hi;
+  return keep_halves(v, !lo, !hi);
+}
+
+// Weights are at most 2^15, so fp16 keeps what is within 2^-39 of the
+// largest weight of its row.
+constexpr float kRwLift = 15.f;
+
+// One step over a 16-position slice of a tile: scores, running maximum and
+// sum, output.  tK, tV: the slice's first row, this kv head; rb: bytes from
+// row to row; sK, sV: the scale bytes of this head in the slice's first row.
+// Key rbase + i is seen by row r when it is <= lim[r] (-1: never).
+// edge: some key of the slice is not seen by some row.  Then V rows that no
+// row sees are zeroed, and infinities and NaN in V are taken out of the
+// product and added to the rows that see them only.
+template <bool FP8>
+__device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4], const float (&rowc)[2],
+                                         const uint8_t* tK, const uint8_t* tV, int rb, const uint8_t* sK,
+                                         const uint8_t* sV, int rbase, const int (&lim)[2], int top, bool edge) {
+  const int lane = threadIdx.x & 31, tg = lane & 3, mtx = lane >> 3;
+  float sc[2][4], sd[2][4];
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[nt][e] = sd[nt][e] = 0.f;
+  float kscale[2][2], vexp[2][2];
+  if constexpr (FP8) {
+    const uint8_t* kr = tK + ((mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
+#pragma unroll
+    for (int c = 0; c < 8; c += 2) {   // 16 keys x 32 codes
+      uint32_t w[4];                   // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
+      ldmatrix_x4(w[0], w[1], w[2], w[3], kr + c * 16);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        mma_f16_16816(sc[nt], qa[c], e4m3x2_to_f16x2(w[nt] & 0xffffu), e4m3x2_to_f16x2(w[nt] >> 16));
+        mma_f16_16816(sd[nt], qa[c + 1], e4m3x2_to_f16x2(w[2 + nt] & 0xffffu), e4m3x2_to_f16x2(w[2 + nt] >> 16));
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = nt * 8 + tg * 2 + e;
+        kscale[nt][e] = e8m0_value(sK[row * rb]);
+        vexp[nt][e] = e8m0_exponent(sV[row * rb]);
+      }
+  } else {
+    const uint8_t* kr = tK + ((mtx >> 1) * 8 + (lane & 7)) * rb + (mtx & 1) * 16;
+#pragma unroll
+    for (int kk = 0; kk < 8; kk += 2) {
+      uint32_t b0, b1, b2, b3, c0, c1, c2, c3;
+      ldmatrix_x4(b0, b1, b2, b3, kr + kk * 32);
+      ldmatrix_x4(c0, c1, c2, c3, kr + kk * 32 + 32);
+      mma_bf16_16816(sc[0], qa[kk], b0, b1);
+      mma_bf16_16816(sc[1], qa[kk], b2, b3);
+      mma_bf16_16816(sd[0], qa[kk + 1], c0, c1);
+      mma_bf16_16816(sd[1], qa[kk + 1], c2, c3);
+    }
+  }
+  // base-2 logits; masked ones are -inf whatever the product was
+  float mx[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
+  float zo[2][4];   // z + log2(scale of v)
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int hh = e >> 1, key = rbase + nt * 8 + tg * 2 + (e & 1);
+      float z = (sc[nt][e] + sd[nt][e]) * rowc[hh];
+      if constexpr (FP8) z *= kscale[nt][e & 1];
+      z = key <= lim[hh] ? z : -INFINITY;
+      sc[nt][e] = z;
+      mx[hh] = fmaxf(mx[hh], z);
+      if constexpr (FP8) {
+        zo[nt][e] = key <= lim[hh] ? z + vexp[nt][e & 1] : -INFINITY;
+        mv[hh] = fmaxf(mv[hh], zo[nt][e]);
+      }
+    }
+  float alpha[2];
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    float v = mx[hh];
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+    const float mnew = fmaxf(st.m[hh], v);
+    const float muse = mnew == -INFINITY ? 0.f : mnew;
+    alpha[hh] = exp2f(st.m[hh] - muse);
+    st.m[hh] = mnew;
+    mx[hh] = muse;
+  }
+  float rsum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float pv = exp2f(sc[nt][e] - mx[e >> 1]);
+      sc[nt][e] = pv;
+      rsum[e >> 1] += pv;
+    }
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    float v = rsum[hh];
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    st.l[hh] = st.l[hh] * alpha[hh] + v;
+  }
+  if constexpr (FP8) {   // the output's own reference and weights
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      float v = mv[hh];
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+      const float mnew = fmaxf(st.mo[hh], v);
+      const float muse = mnew == -INFINITY ? 0.f : mnew;
+      alpha[hh] = exp2f(st.mo[hh] - muse);
+      st.mo[hh] = mnew;
+      mv[hh] = muse - kRwLift;
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[nt][e] = exp2f(zo[nt][e] - mv[e >> 1]);
+  }
+  if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {   // a reference moved
+#pragma unroll
+    for (int dt = 0; dt < 16; ++dt) {
+      st.o[dt][0] *= alpha[0];
+      st.o[dt][1] *= alpha[0];
+      st.o[dt][2] *= alpha[1];
+      st.o[dt][3] *= alpha[1];
+    }
+  }
+  bool bad = false;
+  // V fragment registers hold keys 2 tg, 2 tg + 1 (b0) and those + 8 (b1)
+  const int k0 = rbase + 2 * tg;
+  if constexpr (FP8) {
+    uint32_t pa[4] = {pack_f16x2(sc[0][0], sc[0][1]), pack_f16x2(sc[0][2], sc[0][3]),
+                      pack_f16x2(sc[1][0], sc[1][1]), pack_f16x2(sc[1][2], sc[1][3])};
+    const uint8_t* vr = tV + ((mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
+#pragma unroll
+    for (int c = 0; c < 8; c += 2) {
+      uint32_t w[4];   // transposed: keys 2 tg, 2 tg + 1 x codes 2 gq, 2 gq + 1 of a chunk
+      ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vr + c * 16);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t x0 = __byte_perm(w[2 * i], 0u, 0x3120), x1 = __byte_perm(w[2 * i + 1], 0u, 0x3120);
+        uint32_t b[4] = {e4m3x2_to_f16x2(x0 & 0xffffu), e4m3x2_to_f16x2(x1 & 0xffffu), e4m3x2_to_f16x2(x0 >> 16),
+                         e4m3x2_to_f16x2(x1 >> 16)};
+        if (edge) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int kb = k0 + (h & 1) * 8;
+            b[h] = clean_halves(keep_halves(b[h], kb <= top, kb + 1 <= top), 0x7c00u, bad);
+          }
+        }
+        mma_f16_16816(st.o[2 * (c + i)], pa, b[0], b[1]);
+        mma_f16_16816(st.o[2 * (c + i) + 1], pa, b[2], b[3]);
+      }
+    }
+  } else {
+    uint32_t pa[4] = {pack_bf16x2(sc[0][0], sc[0][1]), pack_bf16x2(sc[0][2], sc[0][3]),
+                      pack_bf16x2(sc[1][0], sc[1][1]), pack_bf16x2(sc[1][2], sc[1][3])};
+    const uint8_t* vr = tV + ((mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
+#pragma unroll
+    for (int dt = 0; dt < 16; dt += 2) {
+      uint32_t b[4];
+      ldmatrix_x4_trans(b[0], b[1], b[2], b[3], vr + dt * 16);
+      if (edge) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int kb = k0 + (h & 1) * 8;
+          b[h] = clean_halves(keep_halves(b[h], kb <= top, kb + 1 <= top), 0x7f80u, bad);
+        }
+      }
+      mma_bf16_16816(st.o[dt], pa, b[0], b[1]);
+      mma_bf16_16816(st.o[dt + 1], pa, b[2], b[3]);
+    }
+  }
+  if (edge && __any_sync(0xffffffffu, bad)) {
+    // rare: infinities and NaN of V reach the rows that see their key
+    for (int i = 0; i < 16; ++i) {
+      if (rbase + i > top) break;
+      const uint8_t* row = tV + (size_t)i * rb;
+#pragma unroll
+      for (int dt = 0; dt < 16; ++dt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // column of st.o[dt][e]: see flush_rows
+          const int d = FP8 ? (dt >> 1) * 16 + 4 * tg + 2 * (e & 1) + (dt & 1) : dt * 8 + 2 * tg + (e & 1);
+          float v;
+          if constexpr (FP8) v = (row[d] & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
+          else v = bf_lo(reinterpret_cast<const uint16_t*>(row)[d]);
+          if (!isfinite(v) && rbase + i <= lim[e >> 1]) st.o[dt][e] += v;
+        }
+    }
+  }
+}
+
+template <bool FP8, bool SPARSE>
+__global__ void __launch_bounds__(kRwThreads, 1)
+paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__ part_o, float* __restrict__ part_ml,
+                       int* __restrict__ err) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + kRwMaxStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + kRwMaxStages);
+  int* sh_plan = const_cast<int*>(abort_flag) + 1;                            // first item and its first tile
+  long long* sh_scan = reinterpret_cast<long long*>(empty + kRwMaxStages + 2);   // 9 words
+  unsigned char* ring = smem + kRwBarBytes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rb = pl.row_bytes, R = pl.R;
+  const size_t stage_bytes = 2 * (size_t)R * rb;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < pl.stages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], kRwConsumers);
+    }
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- the CTA's share [lo, hi) of all tiles, and where it starts
+  const int per = (pl.P + kRwThreads - 1) / kRwThreads;
+  const int p0 = min((int)threadIdx.x * per, pl.P), p1 = min(p0 + per, pl.P);
+  int mine = 0;
+  for (int p = p0; p < p1; ++p) mine += item_tiles<SPARSE>(a, pl, p);
+  long long before;
+  const long long U = block_scan<kRwThreads>(mine, before, sh_scan);
+  const long long Weff = U < pl.W ? U : pl.W;
+  if ((long long)blockIdx.x >= Weff) return;   // fewer tiles than CTAs
+  const long long lo = blockIdx.x * U / Weff, hi = (blockIdx.x + 1) * U / Weff;
+  if (before <= lo && lo < before + mine) {
+    long long at = before;
+    for (int p = p0; p < p1; ++p) {
+      const int n = item_tiles<SPARSE>(a, pl, p);
+      if (lo < at + n) {
+        sh_plan[0] = p;
+        sh_plan[1] = (int)(lo - at);
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  const int capacity = a.max_pages << a.page_shift;
+  int p = sh_plan[0], tile = sh_plan[1];
+  long long left = hi - lo;
+
+  if (warp == kRwConsumers) {
+    // ------------------------------------------------------------ producer
+    uint32_t fill = 0;
+    const int page_mask = (1 << a.page_shift) - 1;
+    bool ok = true;
+    for (; left > 0 && ok; ++p, tile = 0) {
+      const int keys = item_keys<SPARSE>(a, pl, p);
+      const int tiles = (keys + R - 1) / R;
+      const int last = (int)min((long long)tiles, tile + left);
+      if (tile >= last) continue;
+      left -= last - tile;
+      const int b = SPARSE ? p : p / pl.nrb;
+      const int32_t* trow = a.table + (long long)b * a.max_pages;
+      // dense: table entries e0 + lane of the tiles ahead, 32 at a time, the
+      // next 32 loading while these are used; sparse: the positions of the
+      // tile after the next and the pages of the next are loading while a
+      // tile's copies are issued
+      int e0 = 0, pg = 0, pg_next = 0;
+      const int e_last = SPARSE ? 0 : (keys - 1) >> a.page_shift;
+      int jn[4] = {0, 0, 0, 0}, pn[4] = {0, 0, 0, 0}, jnn[4] = {0, 0, 0, 0};
+      const int32_t* irow = SPARSE ? a.idx + (long long)b * a.k : nullptr;
+      auto load_idx = [&](int (&j)[4], int t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i, at = t * R + r;
+          if (r < R && at < keys) {
+            int v = __ldg(irow + at);
+            if (v < 0 || v >= capacity) {
+              paged_note(a.dbg, kDbgPagedIndex, v, capacity);
+              v = v < 0 ? 0 : capacity - 1;
+            }
+            j[i] = v;
+          }
+        }
+      };
+      auto load_pages = [&](int (&g)[4], const int (&j)[4], int t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i;
+          if (r < R && t * R + r < keys) g[i] = __ldg(trow + (j[i] >> a.page_shift));
+        }
+      };
+      if constexpr (SPARSE) {
+        load_idx(jn, tile);
+        load_pages(pn, jn, tile);
+        if (tile + 1 < last) load_idx(jnn, tile + 1);
+      } else {
+        e0 = tile * R >> a.page_shift;
+        pg = e0 + lane <= e_last ? __ldg(trow + e0 + lane) : 0;
+        pg_next = e0 + 32 + lane <= e_last ? __ldg(trow + e0 + 32 + lane) : 0;
+      }
+      for (int t = tile; t < last; ++t) {
+        const int s = (int)(fill % (uint32_t)pl.stages);
+        const uint32_t use = fill / (uint32_t)pl.stages;
+        if (use > 0 && !tc::mbar_wait(&empty[s], (use - 1) & 1u, abort_flag, err, 21)) {
+          ok = false;
+          break;
+        }
+        unsigned char* stK = ring + (size_t)s * stage_bytes;
+        unsigned char* stV = stK + (size_t)R * rb;
+        const int rows = min(R, keys - t * R);   // rows past the last key stay as they are (masked)
+        if (lane == 0) tc::mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)rows * (uint32_t)rb);
+        __syncwarp();
+        if constexpr (SPARSE) {
+          int jc[4], pc[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) jc[i] = jn[i], pc[i] = pn[i], jn[i] = jnn[i];
+          if (t + 1 < last) load_pages(pn, jn, t + 1);
+          if (t + 2 < last) load_idx(jnn, t + 2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = lane + 32 * i;
+            if (r < rows) {
+              const int page = checked_page(pc[i], a.num_pages, a.dbg);
+              const long long off = (((long long)page << a.page_shift) + (jc[i] & page_mask)) * rb;
+              tc::bulk_load(stK + (size_t)r * rb, a.kp + off, (uint32_t)rb, &full[s]);
+              tc::bulk_load(stV + (size_t)r * rb, a.vp + off, (uint32_t)rb, &full[s]);
+            }
+          }
+        } else {
+          // the tile is one piece of a page, or several whole pages
+          const int j0 = t * R;
+          const int piece = min(R, page_mask + 1);
+          const int first = j0 >> a.page_shift, pages = (R + page_mask) >> a.page_shift;
+          if (first >= e0 + 32) {
+            e0 += 32;
+            pg = pg_next;
+            pg_next = e0 + 32 + lane <= e_last ? __ldg(trow + e0 + 32 + lane) : 0;
+          }
+          // (a tile's pages never straddle the window: both are powers of two)
+          const int mine_pg = __shfl_sync(0xffffffffu, pg, (first - e0 + (lane & 15)) & 31);
+          const int pi = lane & 15;
+          const int r0 = pi * piece;
+          if (pi < pages && r0 < rows) {
+            const int page = checked_page(mine_pg, a.num_pages, a.dbg);
+            const int n = min(piece, rows - r0);
+            const long long off = (((long long)page << a.page_shift) + ((j0 + r0) & page_mask)) * rb;
+            if (lane < 16) tc::bulk_load(stK + (size_t)r0 * rb, a.kp + off, (uint32_t)(n * rb), &full[s]);
+            else tc::bulk_load(stV + (size_t)r0 * rb, a.vp + off, (uint32_t)(n * rb), &full[s]);
+          }
+        }
+        ++fill;
+      }
+    }
+    // every copy this CTA issued lands before it exits
+    for (int s = 0; s < pl.stages; ++s) {
+      if ((uint32_t)s < fill) {
+        const uint32_t last_use = (fill - 1 - (uint32_t)s) / (uint32_t)pl.stages;
+        if (!tc::mbar_wait_drain(&full[s], last_use & 1u) && err) atomicCAS(err, 0, 22);
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int gq = lane >> 2, tg = lane & 3;
+  const int hs = warp / pl.wph, rs = warp % pl.wph;
+  const bool active = hs < a.Hkv;
+  RowState st;
+  uint32_t qa[8][4];
+  float rowc[2];
+  uint32_t fill = 0;
+  bool ok = true;
+  for (; left > 0 && ok; ++p, tile = 0) {
+    const int keys = item_keys<SPARSE>(a, pl, p);
+    const int tiles = (keys + R - 1) / R;
+    const int last = (int)min((long long)tiles, tile + left);
+    if (tile >= last) continue;
+    left -= last - tile;
+    int tok0 = p, ntok = 1, lim[2];
+    if constexpr (SPARSE) {
+      lim[0] = lim[1] = keys - 1;
+    } else {
+      const int b = p / pl.nrb, t0 = p % pl.nrb * pl.tb;
+      const SeqSpan s = seq_span(a.q_start, a.kv_len, b, a.N, capacity);
+      tok0 = s.begin + t0;
+      ntok = min(pl.tb, min(s.len, a.max_q) - t0);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) lim[hh] = min(s.pos0 + t0 + (gq + 8 * hh) / a.G, keys - 1);
+    }
+    const int low = SPARSE ? keys - 1 : keys - ntok;   // the least position a row of the block ends at
+    state_init(st);
+    load_q_rows<FP8>(qa, rowc, a, tok0, ntok, hs, active);
+    for (int t = tile; t < last; ++t) {
+      const int s = (int)(fill % (uint32_t)pl.stages);
+      if (!tc::mbar_wait(&full[s], (fill / (uint32_t)pl.stages) & 1u, abort_flag, err, 23)) {
+        ok = false;
+        break;
+      }
+      const int rbase = t * R + rs * 16;
+      if (active && rbase < keys) {
+        const uint8_t* tK = ring + (size_t)s * stage_bytes + (size_t)(rs * 16) * rb;
+        const uint8_t* tV = tK + (size_t)R * rb;
+        const int tail = a.Hkv * kPgD + hs, off = hs * (FP8 ? kPgD : 2 * kPgD);
+        row_step<FP8>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1,
+                      rbase + 15 > low);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&empty[s]);
+      ++fill;
+    }
+    if (active && ok) {
+      // CTA c's partial of item p sits in slot p + c: the CTAs that meet item
+      // p + 1 start at or after the last one that meets p, so slots never collide
+      const long long slot = ((long long)p + blockIdx.x) * pl.wph + rs;
+      const long long base = (slot * a.Hkv + hs) * pl.RB;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = gq + 8 * hh;
+        if (r >= ntok * a.G) continue;
+        float* po = part_o + (base + r) * kPgD;
+        if constexpr (FP8) {
+          // outputs go to the softmax's own reference m
+          const float f = st.mo[hh] == -INFINITY ? 0.f : exp2f(st.mo[hh] - st.m[hh] - kRwLift);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4*>(po + c * 16 + 4 * tg) =
+                make_float4(st.o[2 * c][2 * hh] * f, st.o[2 * c + 1][2 * hh] * f, st.o[2 * c][2 * hh + 1] * f,
+                            st.o[2 * c + 1][2 * hh + 1] * f);
+        } else {
+#pragma unroll
+          for (int dt = 0; dt < 16; ++dt)
+            *reinterpret_cast<float2*>(po + dt * 8 + 2 * tg) = make_float2(st.o[dt][2 * hh], st.o[dt][2 * hh + 1]);
+        }
+        if (tg == 0) *reinterpret_cast<float2*>(part_ml + (base + r) * 2) = make_float2(st.m[hh], st.l[hh]);
+      }
+    }
+  }
+}
+
+// One CTA per (token, query head): out = sum_x w_x o_x / L, w_x = 2^(m_x - M),
+// L = sum_x w_x l_x, M = max_x m_x over the contributors x of its row block.
+template <bool SPARSE>
+__global__ void __launch_bounds__(kRwMergeThreads)
+paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* __restrict__ part_o,
+                             const float* __restrict__ part_ml, const int* __restrict__ err) {
+  constexpr int kWarps = kRwMergeThreads / 32;
+  constexpr int kPre = 16;
+  __shared__ float wts[kRwMergeMaxC];
+  __shared__ float red[kWarps][kPgD];
+  __shared__ float rmax[kWarps], rsum[kWarps];
+  __shared__ long long sh_scan[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tok = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
+  const int hs = h / a.G, gq = h % a.G;
+  int p = tok, row = gq;
+  if constexpr (!SPARSE) {
+    const int b = seq_of_token(a.q_start, a.B, tok);
+    if (b < 0) return;
+    const SeqSpan s = seq_span(a.q_start, a.kv_len, b, a.N, a.max_pages << a.page_shift);
+    const int t = tok - s.begin;
+    if (t >= a.max_q) return;
+    p = b * pl.nrb + t / pl.tb;
+    row = t % pl.tb * a.G + gq;
+  }
+  // tiles before item p and in all
+  long long v = 0, pre_tiles = 0;
+  for (int i = tid; i < pl.P; i += kRwMergeThreads) {
+    const int n = item_tiles<SPARSE>(a, pl, i);
+    v += n;
+    if (i < p) pre_tiles += n;
+  }
+  const int n_p = item_tiles<SPARSE>(a, pl, p);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v += __shfl_xor_sync(0xffffffffu, v, o);
+    pre_tiles += __shfl_xor_sync(0xffffffffu, pre_tiles, o);
+  }
+  __shared__ long long sh_pre[kWarps];
+  if (lane == 0) {
+    sh_scan[warp] = v;
+    sh_pre[warp] = pre_tiles;
+  }
+  __syncthreads();
+  long long U = 0, base_u = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    U += sh_scan[w];
+    base_u += sh_pre[w];
+  }
+  const long long Weff = U < pl.W ? U : pl.W;
+  // the CTA that owns unit u: the largest c with floor(c U / W) <= u
+  const long long first = n_p ? ((base_u + 1) * Weff - 1) / U : 0;
+  const long long last_c = n_p ? ((base_u + n_p) * Weff - 1) / U : -1;
+  const int C = (int)(last_c - first + 1) * pl.wph;
+  const long long xstride = (long long)a.Hkv * pl.RB;   // entries between consecutive contributors
+  const long long e0 = (((long long)p + first) * pl.wph * a.Hkv + hs) * pl.RB + row;
+  const float* pml = part_ml + e0 * 2;
+  const float* po = part_o + e0 * kPgD;
+  pdl_wait();
+  pdl_launch_dependents();
+  const float2 ml0 = tid < C ? __ldcg(reinterpret_cast<const float2*>(pml + (long long)tid * xstride * 2))
+                             : make_float2(-INFINITY, 0.f);
+  float4 pre[kPre];
+#pragma unroll
+  for (int i = 0; i < kPre; ++i) {
+    const int x = warp + kWarps * i;
+    pre[i] = x < C ? __ldcg(reinterpret_cast<const float4*>(po + (long long)x * xstride * kPgD) + lane)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const int failed = *err;
+  float mloc = ml0.x;
+  for (int x = tid + kRwMergeThreads; x < C; x += kRwMergeThreads)
+    mloc = fmaxf(mloc, __ldcg(pml + (long long)x * xstride * 2));
+  mloc = warp_max(mloc);
+  if (lane == 0) rmax[warp] = mloc;
+  __syncthreads();
+  float M = rmax[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) M = fmaxf(M, rmax[w]);
+  // (a NaN sum counts: it belongs in the result)
+  auto weight = [&](float2 ml) { return ml.x != -INFINITY || ml.y != 0.f ? exp2f(ml.x - M) : 0.f; };
+  float lloc = 0.f;
+  if (tid < C) {
+    const float wv = weight(ml0);
+    wts[tid] = wv;
+    lloc = wv != 0.f ? ml0.y * wv : 0.f;
+  }
+  for (int x = tid + kRwMergeThreads; x < C; x += kRwMergeThreads) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(pml + (long long)x * xstride * 2));
+    const float wv = weight(ml);
+    wts[x] = wv;
+    lloc += wv != 0.f ? ml.y * wv : 0.f;
+  }
+  lloc = warp_sum(lloc);
+  if (lane == 0) rsum[warp] = lloc;
+  __syncthreads();
+  float L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) L += rsum[w];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fold = [&](float4 ov, float wt) {
+    if (wt == 0.f) return;
+    acc.x = fmaf(ov.x, wt, acc.x);
+    acc.y = fmaf(ov.y, wt, acc.y);
+    acc.z = fmaf(ov.z, wt, acc.z);
+    acc.w = fmaf(ov.w, wt, acc.w);
+  };
+#pragma unroll
+  for (int i = 0; i < kPre; ++i) {
+    const int x = warp + kWarps * i;
+    if (x < C) fold(pre[i], wts[x]);
+  }
+#pragma unroll 4
+  for (int x = warp + kWarps * kPre; x < C; x += kWarps)
+    fold(__ldcg(reinterpret_cast<const float4*>(po + (long long)x * xstride * kPgD) + lane), wts[x]);
+  *reinterpret_cast<float4*>(&red[warp][lane * 4]) = acc;
+  __syncthreads();
+  if (tid < kPgD) {
+    float o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) o += red[w][tid];
+    const bool none = L == 0.f;   // nothing to attend to
+    const float res = none ? 0.f : o / L;
+    const long long at = (long long)tok * a.Hq + h;
+    // a kernel that gave up leaves NaN, so the failure is visible
+    a.out[at * kPgD + tid] = failed ? (uint16_t)0x7fc0 : (uint16_t)(pack_bf16x2(res, 0.f) & 0xffffu);
+    if (tid == 0 && a.lse != nullptr)
+      a.lse[at] = failed ? __int_as_float(0x7fc00000) : (none ? -INFINITY : (M + log2f(L)) * kPgLn2);
+  }
+}
+
+RowsPlan rows_plan(int fp8, int B, int Hkv, int G, int max_q) {
+  RowsPlan pl;
+  pl.tb = 16 / G < max_q ? 16 / G : max_q;
+  pl.nrb = (max_q + pl.tb - 1) / pl.tb;
+  pl.RB = pl.tb * G;
+  pl.P = B * pl.nrb;
+  pl.wph = kRwConsumers / Hkv;   // 8, 4, 2 or 1 for Hkv <= 8: tiles and pages are powers of two, neither
+  pl.R = 16 * pl.wph;            // straddles the other
+  pl.row_bytes = paged_row_bytes(fp8, Hkv);
+  const int stage = 2 * pl.R * pl.row_bytes;
+  pl.stages = kRwStageBytes / stage < kRwMaxStages ? kRwStageBytes / stage : kRwMaxStages;
+  pl.W = device_sm_count();
+  if (pl.W > kRwMergeMaxC / pl.wph) pl.W = kRwMergeMaxC / pl.wph;
+  return pl;
+}
+
+size_t align256p(size_t x) { return (x + 255) & ~size_t(255); }
+constexpr size_t kRwHead = 256;   // the kernel error word
+
+size_t rows_slots(const RowsPlan& pl, int Hkv) { return (size_t)(pl.P + pl.W) * pl.wph * Hkv * pl.RB; }
+
+template <bool FP8, bool SPARSE>
+cudaError_t launch_rows(const PagedArgs& a, void* ws, cudaStream_t st) {
+  const RowsPlan pl = rows_plan(FP8, a.B, a.Hkv, a.G, SPARSE ? 1 : a.max_q);
+  const size_t slots = rows_slots(pl, a.Hkv);
+  char* p = static_cast<char*>(ws);
+  int* err = reinterpret_cast<int*>(p);
+  float* po = reinterpret_cast<float*>(p + kRwHead);
+  float* pml = reinterpret_cast<float*>(p + kRwHead + align256p(slots * kPgD * 4));
+  const size_t smem = kRwBarBytes + (size_t)pl.stages * 2 * pl.R * pl.row_bytes;
+  auto kern = paged_attn_rows_kernel<FP8, SPARSE>;
+  cudaError_t e = ensure_dynamic_smem((const void*)kern, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3((unsigned)pl.W), dim3(kRwThreads), smem, st, a, pl, po, pml, err);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_attn_rows_merge_kernel<SPARSE>, dim3((unsigned)((long long)a.N * a.Hq)), dim3(kRwMergeThreads),
+                 0, st, a, pl, po, pml, err);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+size_t paged_rows_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q) {
+  const RowsPlan pl = rows_plan(fp8, B, Hkv, G, max_q);
+  const size_t slots = rows_slots(pl, Hkv);
+  return kRwHead + align256p(slots * kPgD * 4) + align256p(slots * 2 * 4);
+}
+
+cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {
+  if (a.N <= 0) return cudaSuccess;
+  if (a.idx != nullptr)
+    return fp8 ? launch_rows<true, true>(a, ws, st) : launch_rows<false, true>(a, ws, st);
+  return fp8 ? launch_rows<true, false>(a, ws, st) : launch_rows<false, false>(a, ws, st);
+}
+
+size_t paged_attn_workspace_bytes(int fp8, int B, int N, int max_q, int Hkv, int G) {
+  (void)N;
+  return paged_rows_workspace_bytes(fp8, B, Hkv, G, max_q);
+}
+
+cudaError_t launch_paged_attn(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {
+  return launch_paged_rows(a, fp8, ws, st);
+}
+
+cudaError_t launch_paged_write(const uint16_t* k_new, const uint16_t* v_new, long long k_stride, long long v_stride,
+                               const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int B, int N,
+                               int max_pages, int num_pages, int page_shift, int Hkv, int fp8, uint8_t* kp,
+                               uint8_t* vp, int* dbg, cudaStream_t st) {
+  if (N <= 0) return cudaSuccess;
+  const dim3 grid((unsigned)((2ll * N + 7) / 8));
+  const cudaError_t e =
+      launch_pdl(fp8 ? paged_write_kernel<true> : paged_write_kernel<false>, grid, dim3(256), 0, st, k_new, v_new,
+                 k_stride, v_stride, q_start, kv_len, table, B, N, max_pages, num_pages, page_shift, Hkv, kp, vp, dbg);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_paged_gather(const uint8_t* kp, const uint8_t* vp, const int32_t* table, const int32_t* idx,
+                                const int32_t* count, int B, int max_pages, int num_pages, int page_shift, int Hkv,
+                                int k, int fp8, uint16_t* ko, uint16_t* vo, int* dbg, cudaStream_t st) {
+  if (B <= 0) return cudaSuccess;
+  const dim3 grid((unsigned)((k + 7) / 8), (unsigned)B);
+  const cudaError_t e = launch_pdl(fp8 ? paged_gather_kernel<true> : paged_gather_kernel<false>, grid, dim3(256), 0,
+                                   st, kp, vp, table, idx, count, max_pages, num_pages, page_shift, Hkv, k, ko, vo,
+                                   dbg);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace sa

@@ -1,0 +1,147 @@
+// Paged K/V cache: what the kernels of paged.cu and paged_tc.cu share.
+//
+// A pool is [num_pages, page_size, row] bytes; a cache row is one position of
+// a sequence, all kv heads, K and V in pools of their own:
+//   bf16   Hkv * 128 bf16 values, 16 zero bytes
+//   E4M3   Hkv * 128 codes, Hkv scale bytes (E8M0: 2^(byte - 127)), zeros to
+//          16 bytes; value = code * 2^(byte - 127)
+// The 16 bytes at the end make a row the layout a tile has in shared memory:
+// rows 16 bytes apart modulo 128 keep ldmatrix free of bank conflicts, so a
+// run of rows is one bulk copy, and the scales travel with their codes.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "sa_common.cuh"
+#include "sa_internal.h"
+
+namespace sa {
+
+constexpr int kPgD = 128;                  // head_dim
+constexpr int kPgPad = 16;                 // bytes at the end of a row
+constexpr float kPgLog2e = 1.4426950408889634f;
+constexpr float kPgLn2 = 0.6931471805599453f;
+
+__host__ __device__ __forceinline__ int paged_row_bytes(int fp8, int Hkv) {
+  return Hkv * kPgD * (fp8 ? 1 : 2) + kPgPad;
+}
+
+// Debug builds record a bad page or position (code, two details) in `rec`
+// (the device debug record) and go on; release builds do nothing.
+__device__ __forceinline__ void paged_note(int* rec, int code, int a, int b) {
+#ifdef SA_DEBUG
+  if (rec != nullptr) {
+    if (atomicCAS(&rec[0], 0, code) == 0) {
+      rec[1] = a;
+      rec[2] = b;
+    }
+    atomicAdd(&rec[3], 1);
+  }
+#else
+  (void)rec, (void)code, (void)a, (void)b;
+#endif
+}
+
+// A page id of a block table, clamped into the pool (a bad one is a caller
+// error: a wrong page is read, nothing faults).
+__device__ __forceinline__ int checked_page(int pg, int num_pages, int* rec) {
+  if (pg < 0 || pg >= num_pages) {
+    paged_note(rec, kDbgPage, pg, num_pages);
+    pg = pg < 0 ? 0 : num_pages - 1;
+  }
+  return pg;
+}
+
+// 2^(byte - 127) as fp32 (E8M0: 255 is NaN).
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7fc00000u : (b == 0u ? 0x00400000u : b << 23));
+}
+// byte - 127 as fp32 (255: NaN).
+__device__ __forceinline__ float e8m0_exponent(uint32_t b) {
+  return b == 255u ? __uint_as_float(0x7fc00000u) : (float)(int)b - 127.f;
+}
+
+// Two E4M3 codes (low byte first) -> two fp16 values, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t lo16) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(lo16));
+  return r;
+}
+// Two fp16 values -> two bf16 values times `s` (each product rounded once).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h, float s) {
+  float a, b;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(a), "=f"(b)
+      : "r"(h));
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b * s), "f"(a * s));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The queries of sequence b: packed tokens [begin, begin + len), token t at
+// position pos0 + t of the kv cached positions.  Whatever q_start and kv_len
+// hold, begin and begin + len stay within [0, N] and kv within the table.
+struct SeqSpan {
+  int begin, len, kv, pos0;
+};
+__device__ __forceinline__ SeqSpan seq_span(const int32_t* __restrict__ q_start, const int32_t* __restrict__ kv_len,
+                                            int b, int N, int capacity) {
+  SeqSpan s;
+  const int a = q_start[b], e = q_start[b + 1], kv = kv_len[b];
+  s.begin = min(max(a, 0), N);
+  s.len = min(max(e, s.begin), N) - s.begin;
+  s.kv = min(max(kv, 0), capacity);
+  s.pos0 = s.kv - s.len;
+  return s;
+}
+
+// The sequence that token i belongs to (all lanes of a warp ask for the same
+// token), or -1: the count of sequences that end at or before i, then a check.
+__device__ __forceinline__ int seq_of_token(const int32_t* __restrict__ q_start, int B, int i) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = B;   // the sequence lies in [lo, hi]
+  while (hi > lo) {     // 32 probes a round: the ends of evenly spaced sequences
+    const int span = hi - lo, step = (span + 31) / 32;
+    const int probe = lo + lane * step + step - 1;
+    const bool past = probe < hi && q_start[probe + 1] <= i;
+    const int n = __popc(__ballot_sync(0xffffffffu, past));
+    lo += n * step;
+    if (lo >= hi) { lo = hi; break; }
+    hi = min(hi, lo + step - 1);
+  }
+  if (lo >= B || q_start[lo] > i || q_start[lo + 1] <= i) return -1;
+  return lo;
+}
+
+// What a paged attention call is given.
+struct PagedArgs {
+  const uint16_t* q = nullptr;      // [N, Hq, 128] bf16, tokens q_stride elements apart
+  long long q_stride = 0;
+  const int32_t* q_start = nullptr; // dense: [B + 1]
+  const int32_t* kv_len = nullptr;  // dense: [B]
+  const int32_t* idx = nullptr;     // sparse: [B, k] positions; count [B]
+  const int32_t* count = nullptr;
+  const uint8_t* kp = nullptr;      // pools
+  const uint8_t* vp = nullptr;
+  const int32_t* table = nullptr;   // [B, max_pages]
+  int B = 0, N = 0, max_q = 0, max_pages = 0, num_pages = 0, page_shift = 0;
+  int Hq = 0, Hkv = 0, G = 0, k = 0;
+  float qscale = 0.f;               // softmax scale * log2(e)
+  uint16_t* out = nullptr;          // [N, Hq, 128]
+  float* lse = nullptr;             // [N, Hq] or null
+  int* dbg = nullptr;               // debug builds: the device debug record
+};
+
+}  // namespace sa

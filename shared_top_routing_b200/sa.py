@@ -25,11 +25,15 @@ SA_ERR_TIMEOUT = 5
 SA_ERR_STALE_INDEX = 6
 SA_MAX_K = 4096
 SA_WS_ALIGN = 256
+SA_KV_BF16 = 0
+SA_KV_E4M3 = 1
+SA_PAGED_MAX_HKV = 8
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
 
 # name -> (restype, argtypes); mirrors include/sa.h
 SIGNATURES = {
@@ -49,6 +53,13 @@ SIGNATURES = {
     "sa_sparse_attn_decode_noalloc": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
     "sa_gather_rows": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
     "sa_sparse_attn_decode_rows": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _Z, _P]),
+    "sa_paged_row_bytes": (_Z, [_I, _I]),
+    "sa_paged_kv_write": (_I, [_P, _P, _L, _L, _P, _P, _P] + [_I] * 8 + [_P, _P, _P]),
+    "sa_paged_kv_gather": (_I, [_P] * 5 + [_I] * 8 + [_P, _P, _P]),
+    "sa_paged_attn_workspace": (_Z, [_I] * 7),
+    "sa_paged_attn": (_I, [_P, _L] + [_P] * 5 + [_I] * 10 + [_F, _P, _P, _P, _Z, _P]),
+    "sa_paged_sparse_attn_decode_workspace": (_Z, [_I] * 6),
+    "sa_paged_sparse_attn_decode": (_I, [_P] * 6 + [_I] * 9 + [_F, _P, _P, _P, _Z, _P]),
     "sa_self_test_bounded_wait": (_I, [_P, ctypes.c_uint32, _P]),
     "sa_gist_route_unfold_workspace": (_Z, [_I, _I, _I, _I]),
     "sa_gist_route_unfold": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P]),
@@ -394,6 +405,241 @@ def sa_sparse_attn_decode_rows(q, k_rows, v_rows, count, scale: float = 0.0, out
                                           scale, _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(),
                                           _stream(stream))
     _check(st, "sa_sparse_attn_decode_rows")
+    return (out, lse) if with_lse else out
+
+
+# ------------------------------------------------------------- paged cache
+
+_D = 128
+
+
+def sa_paged_kv_alloc(num_pages: int, page_size: int, Hkv: int, kv_type: int = SA_KV_BF16, device=None):
+    """Zero-filled K and V pools [num_pages, page_size, row] of a paged cache
+    (see sa.h): bf16 rows of Hkv * 128 + 8 values, or uint8 rows of
+    Hkv * 128 E4M3 codes and 16 bytes of scales."""
+    torch = _torch()
+    nbytes = lib().sa_paged_row_bytes(kv_type, Hkv)
+    if nbytes == 0:
+        raise ValueError(f"no paged cache of kv_type {kv_type} and {Hkv} kv heads (1 to {SA_PAGED_MAX_HKV})")
+    dtype, row = (torch.bfloat16, nbytes // 2) if kv_type == SA_KV_BF16 else (torch.uint8, nbytes)
+    return tuple(torch.zeros((num_pages, page_size, row), dtype=dtype, device=device) for _ in range(2))
+
+
+def _pools(k_pages, v_pages, dev):
+    """(kv_type, Hkv) of a pair of pools: by their element type and row size."""
+    torch = _torch()
+    if k_pages.dtype not in (torch.bfloat16, torch.uint8):
+        raise ValueError("k_pages must be bfloat16, or uint8 for E4M3 rows")
+    if k_pages.dim() != 3 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+        raise ValueError("k_pages and v_pages must be pools [num_pages, page_size, row] of one shape and type")
+    kv_type = SA_KV_BF16 if k_pages.dtype == torch.bfloat16 else SA_KV_E4M3
+    Hkv, rest = divmod(k_pages.shape[2] - (8 if kv_type == SA_KV_BF16 else 16), _D)
+    if rest or Hkv < 1:
+        raise ValueError(f"rows of {k_pages.shape[2]} elements are not a paged cache's (see sa.h)")
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.device != dev:
+            raise ValueError(f"{n} must be on {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    return kv_type, Hkv
+
+
+def _ints32(t, name, dev, shape):
+    if t.dtype != _torch().int32 or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, has {list(t.shape)}")
+
+
+def _tokens(t, name, dev):
+    """Token stride of [N, H, 128] bf16 rows whose heads lie side by side."""
+    if t.dtype != _torch().bfloat16 or not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor on {dev}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [N, heads, {_D}]")
+    H = t.shape[1]
+    if t.shape[2] > 1 and t.stride(2) != 1 or H > 1 and t.stride(1) != t.shape[2]:
+        raise ValueError(f"{name}'s heads must lie side by side in a token")
+    return t.stride(0) if t.shape[0] > 1 else max(8, H * t.shape[2])
+
+
+def _result(t, name, dev, shape, dtype):
+    """An output buffer the caller gave, checked."""
+    if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {dev}")
+
+
+def _call_stream(dev, stream):
+    """(raw stream, context) a call on tensors of `dev` runs on: the given
+    stream, or the current one of that device; the context makes the device
+    (and a given stream, so that outputs belong to it) current."""
+    import contextlib
+    torch = _torch()
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is of {stream.device}, the tensors are on {dev}")
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    if torch.cuda.current_device() != dev.index:
+        return raw, torch.cuda.device(dev)
+    return raw, contextlib.nullcontext()
+
+
+_paged_ws: dict = {}
+
+
+def _paged_workspace(nbytes: int, dev, raw_stream: int):
+    """A workspace for one call on a stream (whose context is current).
+    Outside a capture, one buffer per stream is kept and grows.  A capture
+    gets a buffer of its own from the graph's memory, zeroed by the graph, so
+    that graphs share none with each other or with calls outside."""
+    torch = _torch()
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        buf[:SA_WS_ALIGN].zero_()
+        return buf
+    key = (dev.index, raw_stream)
+    buf = _paged_ws.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        _paged_ws[key] = buf
+    return buf
+
+
+def sa_paged_kv_write(k_new, v_new, k_pages, v_pages, block_table, q_start, kv_len, stream=None):
+    """Writes the new tokens' K and V into the pools, in place (see sa.h).
+
+    k_new, v_new [N, Hkv, 128] bf16 (slices of a fused projection are fine);
+    pools from sa_paged_kv_alloc; block_table [B, max_pages], q_start [B + 1],
+    kv_len [B] int32, kv_len counting the new tokens.  Returns the pools."""
+    dev = k_new.device
+    ks, vs = _tokens(k_new, "k_new", dev), _tokens(v_new, "v_new", dev)
+    kv_type, Hkv = _pools(k_pages, v_pages, dev)
+    N, B = k_new.shape[0], kv_len.shape[0]
+    if k_new.shape != (N, Hkv, _D) or v_new.shape != (N, Hkv, _D):
+        raise ValueError(f"k_new and v_new must have shape [N, {Hkv}, {_D}]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have shape [B, max_pages]")
+    _ints32(block_table, "block_table", dev, (B, block_table.shape[1]))
+    _ints32(q_start, "q_start", dev, (B + 1,))
+    _ints32(kv_len, "kv_len", dev, (B,))
+    raw, ctx = _call_stream(dev, stream)
+    with ctx:
+        st = lib().sa_paged_kv_write(k_new.data_ptr(), v_new.data_ptr(), ks, vs, q_start.data_ptr(),
+                                     kv_len.data_ptr(), block_table.data_ptr(), B, N, block_table.shape[1],
+                                     k_pages.shape[0], k_pages.shape[1], Hkv, _D, kv_type, k_pages.data_ptr(),
+                                     v_pages.data_ptr(), raw)
+    _check(st, "sa_paged_kv_write")
+    return k_pages, v_pages
+
+
+def sa_paged_kv_gather(k_pages, v_pages, block_table, idx, count, k_rows=None, v_rows=None, stream=None):
+    """Selected rows of a paged cache as compact bf16 rows [B, k, Hkv * 128 + 8]
+    (zeros past count), for sa_sparse_attn_decode_rows.  idx [B, k], count [B]."""
+    torch = _torch()
+    dev = k_pages.device
+    kv_type, Hkv = _pools(k_pages, v_pages, dev)
+    if idx.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("idx must have shape [B, k] and block_table [B, max_pages]")
+    B, k = idx.shape
+    _ints32(block_table, "block_table", dev, (B, block_table.shape[1]))
+    _ints32(idx, "idx", dev, (B, k))
+    _ints32(count, "count", dev, (B,))
+    shape = (B, k, Hkv * _D + 8)
+    raw, ctx = _call_stream(dev, stream)
+    with ctx:
+        if k_rows is None:
+            k_rows = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _result(k_rows, "k_rows", dev, shape, torch.bfloat16)
+        if v_rows is None:
+            v_rows = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _result(v_rows, "v_rows", dev, shape, torch.bfloat16)
+        st = lib().sa_paged_kv_gather(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), idx.data_ptr(),
+                                      count.data_ptr(), B, block_table.shape[1], k_pages.shape[0], k_pages.shape[1],
+                                      Hkv, _D, k, kv_type, k_rows.data_ptr(), v_rows.data_ptr(), raw)
+    _check(st, "sa_paged_kv_gather")
+    return k_rows, v_rows
+
+
+def _paged_ws_args(need, ws, dev, raw):
+    if ws is None:
+        ws = _paged_workspace(need, dev, raw) if need else None
+    elif ws.device != dev:
+        raise ValueError(f"ws must be on {dev}")
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def sa_paged_attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q: int | None = None, scale: float = 0.0,
+                  out=None, with_lse: bool = False, ws=None, stream=None):
+    """Attention of a chunk of new tokens per sequence over a paged cache, each
+    token over every position up to its own (see sa.h).
+
+    q [N, Hq, 128] bf16, the sequences' tokens packed by q_start [B + 1];
+    kv_len [B] counts them; max_q bounds the tokens of one sequence (1 for
+    decode; by default N).  Returns out [N, Hq, 128][, lse [N, Hq] fp32]."""
+    torch = _torch()
+    dev = q.device
+    qs = _tokens(q, "q", dev)
+    kv_type, Hkv = _pools(k_pages, v_pages, dev)
+    N, Hq, D = q.shape
+    B = kv_len.shape[0]
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have shape [B, max_pages]")
+    _ints32(block_table, "block_table", dev, (B, block_table.shape[1]))
+    _ints32(q_start, "q_start", dev, (B + 1,))
+    _ints32(kv_len, "kv_len", dev, (B,))
+    max_q = N if max_q is None else max_q
+    raw, ctx = _call_stream(dev, stream)
+    L = lib()
+    with ctx:
+        if out is None:
+            out = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=dev)
+        else:
+            _result(out, "out", dev, (N, Hq, D), torch.bfloat16)
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev) if with_lse else None
+        wp, wn = _paged_ws_args(L.sa_paged_attn_workspace(B, N, max_q, Hq, Hkv, D, kv_type), ws, dev, raw)
+        st = L.sa_paged_attn(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                             q_start.data_ptr(), kv_len.data_ptr(), B, N, max_q, block_table.shape[1],
+                             k_pages.shape[0], k_pages.shape[1], Hq, Hkv, D, kv_type, scale, out.data_ptr(),
+                             None if lse is None else lse.data_ptr(), wp, wn, raw)
+    _check(st, "sa_paged_attn")
+    return (out, lse) if with_lse else out
+
+
+def sa_paged_sparse_attn_decode(q, k_pages, v_pages, block_table, idx, count, scale: float = 0.0, out=None,
+                                with_lse: bool = False, ws=None, stream=None):
+    """sa_sparse_attn_decode over a paged cache: q [B, Hq, 128]; idx [B, k]
+    positions; count [B].  Returns out [B, Hq, 128][, lse [B, Hq] fp32]."""
+    torch = _torch()
+    dev = q.device
+    _tokens(q, "q", dev)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    kv_type, Hkv = _pools(k_pages, v_pages, dev)
+    B, Hq, D = q.shape
+    if idx.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("idx must have shape [B, k] and block_table [B, max_pages]")
+    k = idx.shape[1]
+    _ints32(block_table, "block_table", dev, (B, block_table.shape[1]))
+    _ints32(idx, "idx", dev, (B, k))
+    _ints32(count, "count", dev, (B,))
+    raw, ctx = _call_stream(dev, stream)
+    L = lib()
+    with ctx:
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=dev)
+        else:
+            _result(out, "out", dev, (B, Hq, D), torch.bfloat16)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if with_lse else None
+        wp, wn = _paged_ws_args(L.sa_paged_sparse_attn_decode_workspace(B, Hq, Hkv, D, k, kv_type), ws, dev, raw)
+        st = L.sa_paged_sparse_attn_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                           block_table.data_ptr(), idx.data_ptr(), count.data_ptr(), B,
+                                           block_table.shape[1], k_pages.shape[0], k_pages.shape[1], Hq, Hkv, D, k,
+                                           kv_type, scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                           wp, wn, raw)
+    _check(st, "sa_paged_sparse_attn_decode")
     return (out, lse) if with_lse else out
 
 
