@@ -536,7 +536,7 @@ sa_status sa_paged_kv_write(const void* k_new, const void* v_new, int64_t k_stri
   if (!aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4))
     return fail(SA_ERR_INVALID_ARG, "q_start/kv_len/block_table misaligned");
   int* rec = nullptr;
-  cudaError_t e = sa::dbg_record(&rec);
+  cudaError_t e = sa::paged_dbg_record(&rec);
   if (e != cudaSuccess) return cuda_fail(e, "debug record");
   e = sa::launch_paged_write(static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new), k_stride,
                              v_stride, q_start, kv_len, block_table, B, N, max_pages, num_pages,
@@ -562,7 +562,7 @@ sa_status sa_paged_kv_gather(const void* k_pages, const void* v_pages, const int
   if (!aligned(idx, 4) || !aligned(count, 4) || !aligned(block_table, 4))
     return fail(SA_ERR_INVALID_ARG, "idx/count/block_table misaligned");
   int* rec = nullptr;
-  cudaError_t e = sa::dbg_record(&rec);
+  cudaError_t e = sa::paged_dbg_record(&rec);
   if (e != cudaSuccess) return cuda_fail(e, "debug record");
   e = sa::launch_paged_gather(static_cast<const uint8_t*>(k_pages), static_cast<const uint8_t*>(v_pages), block_table,
                               idx, count, B, max_pages, num_pages, page_shift_of(page_size), Hkv, k,
@@ -619,7 +619,7 @@ sa_status sa_paged_attn(const void* q, int64_t q_stride, const void* k_pages, co
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   cudaStream_t cs = as_cuda(stream);
-  cudaError_t e = sa::dbg_record(&a.dbg);
+  cudaError_t e = sa::paged_dbg_record(&a.dbg);
   if (e != cudaSuccess) return cuda_fail(e, "debug record");
   if ((e = sa::dbg_arm(ws, need - sa::kWsCanary, cs)) != cudaSuccess) return cuda_fail(e, "debug canary");
   if ((e = sa::launch_paged_attn(a, kv_type == SA_KV_E4M3, ws, cs)) != cudaSuccess)
@@ -669,7 +669,7 @@ sa_status sa_paged_sparse_attn_decode(const void* q, const void* k_pages, const 
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   cudaStream_t cs = as_cuda(stream);
-  cudaError_t e = sa::dbg_record(&a.dbg);
+  cudaError_t e = sa::paged_dbg_record(&a.dbg);
   if (e != cudaSuccess) return cuda_fail(e, "debug record");
   if ((e = sa::dbg_arm(ws, need - sa::kWsCanary, cs)) != cudaSuccess) return cuda_fail(e, "debug canary");
   if ((e = sa::launch_paged_rows(a, kv_type == SA_KV_E4M3, ws, cs)) != cudaSuccess)
@@ -845,8 +845,12 @@ sa_status sa_debug_check_canary(const void* ws, size_t offset, int site, sa_stre
 
 sa_status sa_debug_read(int32_t* record, int reset) {
   if (record == nullptr) return fail(SA_ERR_INVALID_ARG, "record is NULL");
-  const cudaError_t e = sa::dbg_read(record, reset != 0);
+  cudaError_t e = sa::dbg_read(record, reset != 0);
   if (e != cudaSuccess) return cuda_fail(e, "debug record read");
+  int paged[4];   // the paged calls keep a record of their own
+  if ((e = sa::paged_dbg_read(paged, reset != 0)) != cudaSuccess) return cuda_fail(e, "debug record read");
+  if (record[0] == 0) std::copy(paged, paged + 3, record);
+  record[3] += paged[3];
   return ok();
 }
 

@@ -946,15 +946,6 @@ cudaError_t dbg_read(int* host4, bool reset) {
 #endif
 }
 
-cudaError_t dbg_record(int** rec) {
-  *rec = nullptr;
-#ifdef SA_DEBUG
-  return cudaGetSymbolAddress(reinterpret_cast<void**>(rec), g_dbg);
-#else
-  return cudaSuccess;
-#endif
-}
-
 cudaError_t launch_attn_prefill(const uint16_t* q, const uint16_t* kc, const uint16_t* vc,
                                 const int32_t* idx, const int32_t* count, int B, int T, int Tk_max,
                                 int Hq, int Hkv, int k, float scale, uint16_t* out, float* lse,

@@ -946,6 +946,34 @@ cudaError_t launch_rows(const PagedArgs& a, void* ws, cudaStream_t st) {
 
 }  // namespace
 
+#ifdef SA_DEBUG
+__device__ int g_paged_dbg[4];
+#endif
+
+cudaError_t paged_dbg_record(int** rec) {
+  *rec = nullptr;
+#ifdef SA_DEBUG
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(rec), g_paged_dbg);
+#else
+  return cudaSuccess;
+#endif
+}
+
+cudaError_t paged_dbg_read(int* host4, bool reset) {
+#ifdef SA_DEBUG
+  cudaError_t e = cudaMemcpyFromSymbol(host4, g_paged_dbg, 4 * sizeof(int));
+  if (e == cudaSuccess && reset) {
+    const int zero[4] = {0, 0, 0, 0};
+    e = cudaMemcpyToSymbol(g_paged_dbg, zero, sizeof(zero));
+  }
+  return e;
+#else
+  (void)reset;
+  for (int i = 0; i < 4; ++i) host4[i] = 0;
+  return cudaSuccess;
+#endif
+}
+
 size_t paged_rows_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q) {
   const RowsPlan pl = rows_plan(fp8, B, Hkv, G, max_q);
   const size_t slots = rows_slots(pl, Hkv);

@@ -28,6 +28,15 @@ __host__ __device__ __forceinline__ int paged_row_bytes(int fp8, int Hkv) {
   return Hkv * kPgD * (fp8 ? 1 : 2) + kPgPad;
 }
 
+// Debug builds: codes of the paged calls' own debug record, which
+// sa_debug_read merges with the library's.
+constexpr int kDbgPage = 5;         // a block table's page outside the pool
+constexpr int kDbgPagedIndex = 6;   // a selected position outside the block table
+// The record's device address on the current device, and its copy (cleared
+// when asked to); null and zeros in release builds.
+cudaError_t paged_dbg_record(int** rec);
+cudaError_t paged_dbg_read(int* host4, bool reset);
+
 // Debug builds record a bad page or position (code, two details) in `rec`
 // (the device debug record) and go on; release builds do nothing.
 __device__ __forceinline__ void paged_note(int* rec, int code, int a, int b) {
@@ -143,5 +152,21 @@ struct PagedArgs {
   float* lse = nullptr;             // [N, Hq] or null
   int* dbg = nullptr;               // debug builds: the device debug record
 };
+
+// Launchers (paged.cu).
+cudaError_t launch_paged_write(const uint16_t* k_new, const uint16_t* v_new, long long k_stride, long long v_stride,
+                               const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int B, int N,
+                               int max_pages, int num_pages, int page_shift, int Hkv, int fp8, uint8_t* kp,
+                               uint8_t* vp, int* dbg, cudaStream_t st);
+cudaError_t launch_paged_gather(const uint8_t* kp, const uint8_t* vp, const int32_t* table, const int32_t* idx,
+                                const int32_t* count, int B, int max_pages, int num_pages, int page_shift, int Hkv,
+                                int k, int fp8, uint16_t* ko, uint16_t* vo, int* dbg, cudaStream_t st);
+// Attention of few query rows per kv head (idx set: one token per sequence
+// over selected rows; else a chunk of at most max_q tokens per sequence).
+size_t paged_rows_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q);
+cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
+// Chunk attention: picks the kernel for the chunk's length.
+size_t paged_attn_workspace_bytes(int fp8, int B, int N, int max_q, int Hkv, int G);
+cudaError_t launch_paged_attn(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
 
 }  // namespace sa

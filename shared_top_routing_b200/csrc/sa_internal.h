@@ -34,8 +34,6 @@ constexpr int kDbgPrefillIndex = 1;
 constexpr int kDbgDecodeIndex = 2;
 constexpr int kDbgGatherIndex = 3;
 constexpr int kDbgCanary = 4;
-constexpr int kDbgPage = 5;         // a block table's page outside the pool
-constexpr int kDbgPagedIndex = 6;   // a selected position outside the block table
 constexpr int kDbgCanaryBytes = 256;
 constexpr unsigned char kDbgCanaryByte = 0xA5;
 #ifdef SA_DEBUG
@@ -49,8 +47,6 @@ constexpr size_t kWsCanary = 0;
 cudaError_t dbg_arm(void* ws, size_t off, cudaStream_t st);
 cudaError_t dbg_check(const void* ws, size_t off, int site, cudaStream_t st);
 cudaError_t dbg_read(int* host4, bool reset);
-// The record's device address on the current device (null in release builds).
-cudaError_t dbg_record(int** rec);
 
 // Rows whose histograms live in the fixed, self-cleaning workspace region.
 constexpr int kHistRowsFixed = 64;
@@ -205,22 +201,5 @@ cudaError_t launch_attn_prefill(const uint16_t* q, const uint16_t* kc, const uin
                                 const int32_t* idx, const int32_t* count, int B, int T, int Tk_max,
                                 int Hq, int Hkv, int k, float scale, uint16_t* out, float* lse,
                                 cudaStream_t st);
-
-// Paged K/V cache (paged.cu, paged_tc.cu; structures in paged.cuh).
-struct PagedArgs;
-cudaError_t launch_paged_write(const uint16_t* k_new, const uint16_t* v_new, long long k_stride, long long v_stride,
-                               const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int B, int N,
-                               int max_pages, int num_pages, int page_shift, int Hkv, int fp8, uint8_t* kp,
-                               uint8_t* vp, int* dbg, cudaStream_t st);
-cudaError_t launch_paged_gather(const uint8_t* kp, const uint8_t* vp, const int32_t* table, const int32_t* idx,
-                                const int32_t* count, int B, int max_pages, int num_pages, int page_shift, int Hkv,
-                                int k, int fp8, uint16_t* ko, uint16_t* vo, int* dbg, cudaStream_t st);
-// Attention of few query rows per kv head (idx set: one token per sequence
-// over selected rows; else a chunk of at most max_q tokens per sequence).
-size_t paged_rows_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q);
-cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
-// Chunk attention: picks the kernel for the chunk's length.
-size_t paged_attn_workspace_bytes(int fp8, int B, int N, int max_q, int Hkv, int G);
-cudaError_t launch_paged_attn(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
 
 }  // namespace sa
