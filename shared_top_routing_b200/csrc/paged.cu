@@ -636,7 +636,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
       for (int t = tile; t < last; ++t) {
         const int s = (int)(fill % (uint32_t)pl.stages);
         const uint32_t use = fill / (uint32_t)pl.stages;
-        if (use > 0 && !tc::mbar_wait(&empty[s], (use - 1) & 1u, abort_flag, err, 21)) {
+        if (use > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&empty[s], (use - 1) & 1u, abort_flag, err, 21))) {
           ok = false;
           break;
         }
@@ -727,7 +727,8 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
     load_q_rows<FP8>(qa, rowc, a, tok0, ntok, hs, active);
     for (int t = tile; t < last; ++t) {
       const int s = (int)(fill % (uint32_t)pl.stages);
-      if (!tc::mbar_wait(&full[s], (fill / (uint32_t)pl.stages) & 1u, abort_flag, err, 23)) {
+      if (!__all_sync(0xffffffffu,
+                      tc::mbar_wait(&full[s], (fill / (uint32_t)pl.stages) & 1u, abort_flag, err, 23))) {
         ok = false;
         break;
       }
@@ -987,13 +988,18 @@ cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_
   return fp8 ? launch_rows<true, false>(a, ws, st) : launch_rows<false, false>(a, ws, st);
 }
 
+// One 16-row block per kv head holds the whole chunk: the row kernel reads
+// the cache once and is bound by HBM.  Longer chunks go to the tensor cores.
+static bool use_rows(int G, int max_q) { return max_q * G <= 16; }
+
 size_t paged_attn_workspace_bytes(int fp8, int B, int N, int max_q, int Hkv, int G) {
   (void)N;
-  return paged_rows_workspace_bytes(fp8, B, Hkv, G, max_q);
+  return use_rows(G, max_q) ? paged_rows_workspace_bytes(fp8, B, Hkv, G, max_q)
+                            : paged_tc_workspace_bytes(B, G, max_q);
 }
 
 cudaError_t launch_paged_attn(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {
-  return launch_paged_rows(a, fp8, ws, st);
+  return use_rows(a.G, a.max_q) ? launch_paged_rows(a, fp8, ws, st) : launch_paged_tc(a, fp8, ws, st);
 }
 
 cudaError_t launch_paged_write(const uint16_t* k_new, const uint16_t* v_new, long long k_stride, long long v_stride,

@@ -1,0 +1,1046 @@
+// Attention of a chunk of new tokens over the paged cache on the tensor cores
+// (tcgen05, sm_100a): many query rows per kv head.
+//
+// Mathematics: out_t = sum_{j <= p_t} softmax_j(scale q_t.k_j) v_j, one pass
+// over the keys in tiles of 128 with a running maximum m and sum l per row:
+// S = Q K^T, P = 2^((S - m) c), l += sum P, O += P V (c = scale * log2 e);
+// when m rises, l and O are scaled by 2^((m_old - m) c).  O is scaled only
+// when the maximum rises by more than 2^8 (the sums stay far inside fp32 and
+// P, at most 2^8, keeps its relative precision in bf16).
+//
+// Rows: the G query heads of a kv head times 128 / G tokens share a 128-row
+// tile (they read the same keys); an item is two such tiles, A and B, of one
+// sequence and kv head, with the key tiles up to its last token.  The two
+// tiles alternate: while one's scores go through the softmax, the tensor core
+// works for the other.  An item with tokens for one tile only lets A take its
+// even key tiles and B its odd ones, and joins them at the end.  The key
+// tiles of all items form one list, cut evenly over one CTA per SM (an item
+// cut in pieces is joined by paged_tc_merge_kernel), so ragged batches and
+// few long sequences load every SM alike.
+//
+// Bound: 4 * 128 flops per (row, key) on the tensor core, and the same number
+// of clocks for the exponentials (128 x 256 of them per key tile at 16 per
+// clock and SM, against 2048 clocks of MMA).
+//
+// CTA of 512 threads, registers moved to the softmax warps (setmaxnreg):
+//   warps 0-3, 4-7   softmax of tile A, of tile B: one thread per row
+//   warp 8           K and V tiles by TMA, a page (or half of one) at a time
+//   warp 9           MMA issue; S and O in TMEM, P over S as the A operand
+//   warp 10          Q tiles by TMA
+//   warps 12-15      E4M3: codes to bf16 (exact) in the operand layout; both:
+//                    V rows no token of the item sees are zeroed, infinities
+//                    and NaN in rows only some see are taken out and added
+//                    to those rows' results at the end
+#include <cudaTypedefs.h>
+
+#include <climits>
+#include <cstddef>
+#include <mutex>
+
+#include "paged.cuh"
+#include "tc_common.cuh"
+
+namespace sa {
+namespace {
+
+using namespace tc;
+
+constexpr int kTcThreads = 512;
+constexpr int kTile = 128;                      // rows of a q tile, keys of a key tile
+constexpr uint32_t kHalfBytes = kTile * 128;    // 64 elements of 128 rows
+constexpr uint32_t kTileBytes = 2 * kHalfBytes; // 128 x 128 bf16
+constexpr int kStages = 2;
+constexpr uint32_t kRawBytes = kTile * 128;     // 128 rows of codes
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;   // 2 * 184 + 2 * 72 = 4 * 128 per warpgroup at launch
+constexpr int kBadRing = 8;                     // items whose bad-row masks are kept
+constexpr int kBadTiles = 3;                    // key tiles a token of an item may not see in full
+
+struct TcPlan {
+  int tpt, tpi, nqb, P;   // tokens per tile and item, items per sequence at most, items per kv head
+  int W;                  // CTAs
+};
+
+struct TcBars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_clean[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t rk_full, rk_empty, rv_full, rv_empty;   // E4M3: raw code tiles
+  uint64_t drain;
+  alignas(16) uint32_t bad[kBadRing][kBadTiles][4];   // V rows with infinities or NaN, by key (read 16 bytes a time)
+  long long scan[kTcThreads / 32];
+  int plan[4];
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(TcBars) <= 1024 && offsetof(TcBars, bad) % 16 == 0 && offsetof(TcBars, scan) % 8 == 0,
+              "barrier block");
+
+template <bool FP8>
+constexpr size_t tc_smem() {
+  return 1024 + 2 * kTileBytes + 2 * kStages * kTileBytes + (FP8 ? 2 * kRawBytes : 0) + 1024;
+}
+
+// What a CTA's first piece is, for the merge.
+struct TcPiece {
+  int b, qb, kvh, j0, j1, n, valid, pad;
+};
+
+// A piece of an item: sequence b, block qb of tpi tokens, kv head, key tiles
+// [j0, j1) of its n.
+struct TcItem {
+  int b, qb, kvh;
+  int tok0, ntA, ntB;   // first token (packed), tokens of tile A and B
+  int pos0, top;        // position of the first token, keys the last one sees
+  int n, j0, j1;
+  int cntA, cntB;       // key tiles of A and B
+  bool split;           // B's rows are A's, over the odd key tiles
+  __device__ __forceinline__ int tile_of(int x, int i) const { return split ? j0 + 2 * i + x : j0 + i; }
+  // first key tile that some token does not see in full
+  __device__ __forceinline__ int first_masked() const { return pos0 < 0 ? 0 : (pos0 + 1) / kTile; }
+};
+
+// Tokens of block qb, and the key tiles up to its last; 0 when it has none.
+__device__ __forceinline__ int item_span(const PagedArgs& a, const TcPlan& pl, int b, int qb, SeqSpan& s, int& nt) {
+  s = seq_span(a.q_start, a.kv_len, b, a.N, a.max_pages << a.page_shift);
+  const int n = min(s.len, a.max_q), t0 = qb * pl.tpi;
+  nt = min(pl.tpi, n - t0);
+  if (nt <= 0) return 0;
+  return max(1, (max(s.pos0 + t0 + nt, 0) + kTile - 1) / kTile);
+}
+
+struct TcIter {
+  int b, qb, kvh, j0;
+  long long left;
+};
+
+__device__ __forceinline__ bool next_item(const PagedArgs& a, const TcPlan& pl, TcIter& c, TcItem& it) {
+  while (c.left > 0 && c.kvh < a.Hkv) {
+    SeqSpan s;
+    int nt;
+    const int n = item_span(a, pl, c.b, c.qb, s, nt);
+    if (n == 0) {
+      c.qb = 0;
+      if (++c.b == a.B) c.b = 0, ++c.kvh;
+      continue;
+    }
+    it.b = c.b, it.qb = c.qb, it.kvh = c.kvh;
+    it.tok0 = s.begin + c.qb * pl.tpi;
+    it.pos0 = s.pos0 + c.qb * pl.tpi;
+    it.ntA = min(nt, pl.tpt);
+    it.ntB = nt - it.ntA;
+    it.top = max(it.pos0 + nt, 0);
+    it.n = n;
+    it.j0 = c.j0;
+    it.j1 = (int)min((long long)n, c.j0 + c.left);
+    it.split = it.ntB == 0;
+    const int len = it.j1 - it.j0;
+    if (it.split) {
+      it.cntA = (len + 1) / 2;
+      it.cntB = len / 2;
+    } else {
+      const int nA = max(1, (max(it.pos0 + it.ntA, 0) + kTile - 1) / kTile);
+      it.cntA = max(0, min(it.j1, nA) - it.j0);
+      it.cntB = len;
+    }
+    c.left -= len;
+    c.j0 = 0;
+    if (++c.qb == pl.nqb) {
+      c.qb = 0;
+      if (++c.b == a.B) c.b = 0, ++c.kvh;
+    }
+    return true;
+  }
+  return false;
+}
+
+// ---- instruction wrappers -------------------------------------------------
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 in, fp32 accumulate.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptor of an operand whose reduction index runs over rows of 128
+// swizzled bytes (64 elements of the other index): 8-row groups 1024 bytes
+// apart, the next 64 elements kHalfBytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
+  d |= (uint64_t)(kHalfBytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two fp32 operations in one instruction (sm_100).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A position's row in the pools: its offset in bytes.
+__device__ __forceinline__ long long row_offset(const int32_t* __restrict__ trow, int pos, int page_shift,
+                                                int num_pages, int rb, int* dbg) {
+  const int pg = checked_page(__ldg(trow + (pos >> page_shift)), num_pages, dbg);
+  return (((long long)pg << page_shift) + (pos & ((1 << page_shift) - 1))) * rb;
+}
+
+// Rare: adds the infinities and NaN of the flagged V rows a token sees to its
+// finished row (bf16) or partial row (fp32), whichever is given.
+template <bool FP8>
+__device__ __noinline__ void add_bad_rows(const uint8_t* __restrict__ vp, const int32_t* __restrict__ trow, int Hkv,
+                                          int kvh, int page_shift, int num_pages, int first_masked,
+                                          const uint32_t* bad, int limit, uint16_t* out, float* part) {
+  const int rb = paged_row_bytes(FP8, Hkv);
+  for (int i = 0; i < kBadTiles * kTile; ++i) {
+    const int key = first_masked * kTile + i;
+    if (key > limit) break;
+    if (!((bad[i >> 5] >> (i & 31)) & 1u)) continue;
+    const uint8_t* row = vp + row_offset(trow, key, page_shift, num_pages, rb, nullptr);
+    const bool whole = FP8 && row[Hkv * kPgD + kvh] == 255;   // the scale is NaN
+    for (int d = 0; d < kPgD; ++d) {
+      float v;
+      if constexpr (FP8)
+        v = whole || (row[kvh * kPgD + d] & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
+      else
+        v = bf_lo(reinterpret_cast<const uint16_t*>(row)[kvh * kPgD + d]);
+      if (isfinite(v)) continue;
+      if (out) out[d] = (uint16_t)(pack_bf16x2(bf_lo(out[d]) + v, 0.f) & 0xffffu);
+      else part[d] += v;
+    }
+  }
+}
+
+// A wait of a whole warp: every lane gets one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                          int code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code));
+}
+
+// ------------------------------------------------------------------ softmax
+
+template <bool FP8>
+__device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, const TcPlan& pl, TcIter c, TcBars& bars,
+                                             volatile int* abort_flag, int* err, float* part_o, float* part_ml,
+                                             float* scratch, uint32_t tmem) {
+  const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const uint32_t lanes = (uint32_t)(row & ~31) << 16;
+  const uint32_t tS = tmem + x * kTile + lanes, tO = tmem + 2 * kTile + x * kTile + lanes;
+  const float qs = a.qscale, lazy = fminf(8.f / qs, 1e30f);
+  const int tr = row / a.G;   // this row's token in the tile
+  const bool fits = row < pl.tpt * a.G;
+  uint32_t ns = 0, no = 0, items = 0;
+  TcItem it;
+  for (; next_item(a, pl, c, it); ++items) {
+    const int cnt = x ? it.cntB : it.cntA;
+    const int nt = x && !it.split ? it.ntB : it.ntA;
+    const int t = (x && !it.split ? pl.tpt : 0) + tr;   // token within the item
+    const bool rowok = fits && tr < nt;
+    const int limit = it.pos0 + t;
+    const bool any = __any_sync(0xffffffffu, rowok);
+    const int wmin = __reduce_min_sync(0xffffffffu, rowok ? limit : INT_MAX);
+    float m = -INFINITY, l = 0.f;
+    bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
+    for (int i = 0; i < cnt; ++i) {
+      const int kb = it.tile_of(x, i) * kTile;
+      ok = warp_wait(&bars.s_full[x], ns & 1u, abort_flag, err, 34) && ok;
+      ++ns;
+      if (ok && any) {
+        tc_fence_after();
+        float s[kTile];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, reinterpret_cast<uint32_t*>(s) + 32 * q);
+        tmem_ld_wait();
+        if (kb + kTile - 1 > wmin) {
+          const int last = limit - kb;
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) s[e] = e <= last ? s[e] : -INFINITY;
+        }
+        float m4[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m4[q] = fmaxf(fmaxf(s[q], s[q + 4]), s[q + 8]);
+#pragma unroll
+        for (int e = 12; e < kTile - 4; e += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) m4[q] = fmaxf(fmaxf(m4[q], s[e + q]), s[e + 4 + q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], s[kTile - 4 + q]);
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const bool up = mx > m + lazy;
+        if (i > 0 && __any_sync(0xffffffffu, up)) {
+          const float f = up ? ex2((m - mx) * qs) : 1.f;   // 0 when nothing was seen before
+          l *= f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * q, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(tO + 32 * q, o);
+          }
+        }
+        if (up) m = mx;
+        const float nm = m == -INFINITY ? 0.f : -m * qs;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float2 v = fma2(make_float2(s[64 * h + 2 * e], s[64 * h + 2 * e + 1]), make_float2(qs, qs),
+                            make_float2(nm, nm));
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            sum[e & 1] = add2(sum[e & 1], v);
+            p[e] = pack_bf16x2(v.x, v.y);
+          }
+          tmem_st32(tS + 32 * h, p);
+        }
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.p_full[x]);
+    }
+    if (cnt > 0) {
+      ok = warp_wait(&bars.o_full[x], no & 1u, abort_flag, err, 35) && ok;
+      ++no;
+      tc_fence_after();
+    }
+    const bool direct = it.j0 == 0 && it.j1 == it.n;
+    const bool join = it.split && it.cntB > 0;
+    float m2 = m == -INFINITY ? -INFINITY : m * qs;   // base-2 logarithm
+    if (x && it.split) {
+      if (join) {   // B's share goes to A through the CTA's scratch rows
+        if (ok && any) {
+          float* dst = scratch + (size_t)row * (kPgD + 4);
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * q, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(dst + 32 * q)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          *reinterpret_cast<float2*>(dst + kPgD) = make_float2(m2, l);
+        }
+        tc_fence_before();
+        named_sync(1, 256);
+        named_sync(2, 256);
+      }
+      continue;
+    }
+    float fA = 1.f, fB = 0.f;
+    const float* other = scratch + (size_t)row * (kPgD + 4);
+    if (join) {
+      named_sync(1, 256);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(other + kPgD));
+      const float mb = ml.x, M = fmaxf(m2, mb);
+      fA = m2 == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m2 - M);
+      fB = mb == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(mb - M);
+      l = (fA != 0.f ? l * fA : 0.f) + (fB != 0.f ? ml.y * fB : 0.f);
+      m2 = M;
+    }
+    const int tok = it.tok0 + t, head = it.kvh * a.G + row % a.G;
+    uint16_t* orow = a.out + ((long long)tok * a.Hq + head) * kPgD;
+    // the piece's slot: 0 continues an item of the CTAs before, 1 is continued by the next
+    const long long slot = 2ll * blockIdx.x + (it.j0 > 0 ? 0 : 1);
+    float* prow = part_o + (slot * 2 * kTile + x * kTile + row) * kPgD;
+    if (direct) {
+      const bool none = l == 0.f;
+      const float inv = none ? 0.f : 1.f / l;
+      fA *= inv;
+      fB *= inv;
+    }
+    const bool dead = fA == 0.f;   // nothing seen: what O holds does not count
+    if (any) {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * q, o);
+        tmem_ld_wait();
+        if (rowok) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float v = __uint_as_float(o[e]);
+          o[e] = __float_as_uint(!ok ? __uint_as_float(0x7fc00000u) : dead || cnt == 0 ? 0.f : v * fA);
+        }
+        if (join && fB != 0.f) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(other + 32 * q) + e);
+            o[4 * e] = __float_as_uint(fmaf(v.x, fB, __uint_as_float(o[4 * e])));
+            o[4 * e + 1] = __float_as_uint(fmaf(v.y, fB, __uint_as_float(o[4 * e + 1])));
+            o[4 * e + 2] = __float_as_uint(fmaf(v.z, fB, __uint_as_float(o[4 * e + 2])));
+            o[4 * e + 3] = __float_as_uint(fmaf(v.w, fB, __uint_as_float(o[4 * e + 3])));
+          }
+        }
+        if (direct) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * u]), __uint_as_float(o[8 * e + 2 * u + 1]));
+            reinterpret_cast<uint4*>(orow + 32 * q)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(prow + 32 * q)[e] =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+        }
+        __syncwarp();
+      }
+    }
+    if (rowok) {
+      if (!direct)
+        *reinterpret_cast<float2*>(part_ml + (slot * 2 * kTile + x * kTile + row) * 2) = make_float2(m2, l);
+      else if (a.lse != nullptr)
+        a.lse[(long long)tok * a.Hq + head] =
+            !ok ? __uint_as_float(0x7fc00000u) : (l == 0.f ? -INFINITY : (m2 + log2f(l)) * kPgLn2);
+      const uint32_t(*bad)[4] = bars.bad[items % kBadRing];
+      uint32_t flagged = 0u;
+#pragma unroll
+      for (int e = 0; e < kBadTiles; ++e) {
+        const uint4 w = *reinterpret_cast<const uint4*>(bad[e]);
+        flagged |= w.x | w.y | w.z | w.w;
+      }
+      if (flagged && ok)
+        add_bad_rows<FP8>(a.vp, a.table + (long long)it.b * a.max_pages, a.Hkv, it.kvh, a.page_shift, a.num_pages,
+                          it.first_masked(), bad[0], limit, direct ? orow : nullptr, prow);
+    }
+    tc_fence_before();   // O is read before the next item's first product overwrites it
+    if (join) named_sync(2, 256);
+  }
+}
+
+// --------------------------------------------------------------------- MMA
+
+__device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, TcIter c, TcBars& bars,
+                                         volatile int* abort_flag, int* err, unsigned char* sQ, unsigned char* sK,
+                                         unsigned char* sV, uint32_t tmem, const bool fp8) {
+  constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kTile);
+  constexpr uint32_t kIdO = kIdS | (1u << 16);   // V: the reduction index is the row
+  uint32_t seq0 = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean = 0u;
+  TcItem it;
+  bool ok = true;
+  auto qk = [&](int x, int i) -> bool {
+    const uint32_t seq = seq0 + (uint32_t)(it.tile_of(x, i) - it.j0);
+    const uint32_t s = seq % kStages;
+    if (!mbar_wait(&bars.k_full[s], (seq / kStages) & 1u, abort_flag, err, 36)) return false;
+    tc_fence_after();
+    const uint32_t qa = smem_u32(sQ) + (x && !it.split ? kTileBytes : 0u), ka = smem_u32(sK) + s * kTileBytes;
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      const uint32_t off = (uint32_t)(ks >> 2) * kHalfBytes + (uint32_t)(ks & 3) * 32u;
+      umma_bf16(tmem + x * kTile, sdesc_k_sw128(qa + off), sdesc_k_sw128(ka + off), kIdS, ks > 0);
+    }
+    umma_commit(&bars.s_full[x]);
+    if (x || it.split) umma_commit(&bars.k_empty[s]);
+    return true;
+  };
+  while (ok && next_item(a, pl, c, it)) {
+    const int cnt[2] = {it.cntA, it.cntB};
+    const int most = max(cnt[0], cnt[1]);
+    const int first_masked = it.first_masked();
+    if (cnt[0] > 0) {
+      if (!mbar_wait(&bars.q_full[0], nq[0] & 1u, abort_flag, err, 37)) break;
+      ++nq[0];
+    }
+    if (!it.split) {
+      if (!mbar_wait(&bars.q_full[1], nq[1] & 1u, abort_flag, err, 37)) break;
+      ++nq[1];
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (ok && cnt[x] > 0) ok = qk(x, 0);
+    for (int i = 0; i < most && ok; ++i) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (i >= cnt[x] || !ok) continue;
+        const int j = it.tile_of(x, i);
+        const uint32_t seq = seq0 + (uint32_t)(j - it.j0), s = seq % kStages;
+        ok = mbar_wait(&bars.v_full[s], (seq / kStages) & 1u, abort_flag, err, 38);
+        if (ok && !fp8 && j >= first_masked) {
+          // cleaned once per tile: A waits (its pair B needs no wait of its own
+          // unless A has no such tile)
+          const bool mine = it.split || x == 0 || i >= cnt[0];
+          if (mine) {
+            ok = mbar_wait(&bars.v_clean[s], (clean >> s) & 1u, abort_flag, err, 39);
+            clean ^= 1u << s;
+          }
+        }
+        ok = ok && mbar_wait(&bars.p_full[x], np[x] & 1u, abort_flag, err, 40);
+        if (!ok) break;
+        ++np[x];
+        tc_fence_after();
+        const uint32_t va = smem_u32(sV) + s * kTileBytes;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          umma_bf16_ts(tmem + 2 * kTile + x * kTile, tmem + x * kTile + ks * 8, sdesc_mn_sw128(va + ks * 2048u), kIdO,
+                       i > 0 || ks > 0);
+        if (x || it.split) umma_commit(&bars.v_empty[s]);
+        if (i + 1 == cnt[x]) {
+          umma_commit(&bars.o_full[x]);
+        } else {
+          ok = qk(x, i + 1);
+        }
+        // Q is free once its last scores are done
+        if (ok && !it.split && i + 2 == cnt[x]) umma_commit(&bars.q_empty[x]);
+        if (ok && !it.split && cnt[x] == 1) umma_commit(&bars.q_empty[x]);
+        if (ok && it.split && i + 1 == cnt[0] && x == 0) umma_commit(&bars.q_empty[0]);
+      }
+    }
+    seq0 += (uint32_t)(it.j1 - it.j0);
+  }
+  // (after an abort) everything issued is done before TMEM is freed
+  if (!ok || *abort_flag) {
+    umma_commit(&bars.drain);
+    if (!mbar_wait_drain(&bars.drain, 0) && err) atomicCAS(err, 0, 41);
+  }
+}
+
+// ------------------------------------------------------------------- kernel
+
+template <bool FP8>
+__global__ void __launch_bounds__(kTcThreads, 1)
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const PagedArgs a, const TcPlan pl,
+                     TcPiece* __restrict__ pieces, float* __restrict__ part_o, float* __restrict__ part_ml,
+                     float* __restrict__ scratch, int* __restrict__ err) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  unsigned char* sQ = base;                                   // tiles A, B
+  unsigned char* sK = sQ + 2 * kTileBytes;
+  unsigned char* sV = sK + kStages * kTileBytes;
+  unsigned char* sRaw = sV + kStages * kTileBytes;            // E4M3: K codes, V codes
+  TcBars& bars = *reinterpret_cast<TcBars*>(sRaw + (FP8 ? 2 * kRawBytes : 0));
+  volatile int* abort_flag = &bars.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.q_full[i], 1);
+      mbar_init(&bars.q_empty[i], 1);
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], 4);
+      mbar_init(&bars.o_full[i], 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bars.k_full[i], FP8 ? 4 : 1);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_full[i], FP8 ? 4 : 1);
+      mbar_init(&bars.v_empty[i], 1);
+      mbar_init(&bars.v_clean[i], 4);
+    }
+    mbar_init(&bars.rk_full, 1);
+    mbar_init(&bars.rk_empty, 4);
+    mbar_init(&bars.rv_full, 1);
+    mbar_init(&bars.rv_empty, 4);
+    mbar_init(&bars.drain, 1);
+    bars.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&bars.tmem_base, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- this CTA's share of the key tiles of all items, kv heads outermost
+  SeqSpan sp;
+  int nt;
+  const int per = (pl.P + kTcThreads - 1) / kTcThreads;
+  const int p0 = min((int)threadIdx.x * per, pl.P), p1 = min(p0 + per, pl.P);
+  int mine = 0;
+  for (int p = p0; p < p1; ++p) mine += item_span(a, pl, p / pl.nqb, p % pl.nqb, sp, nt);
+  long long before = 0, S = 0;
+  {
+    long long v = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) bars.scan[warp] = v;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+#pragma unroll
+    for (int w = 0; w < kTcThreads / 32; ++w) {
+      if (w < warp) before += bars.scan[w];
+      S += bars.scan[w];
+    }
+    before += v - mine;
+  }
+  const long long U = S * a.Hkv, Weff = U < pl.W ? U : pl.W;
+  const bool idle = (long long)blockIdx.x >= Weff;
+  const long long lo = idle ? 0 : blockIdx.x * U / Weff, hi = idle ? 0 : (blockIdx.x + 1) * U / Weff;
+  const long long r = idle ? 0 : lo % S;
+  if (!idle && before <= r && r < before + mine) {
+    long long at = before;
+    for (int p = p0; p < p1; ++p) {
+      const int n = item_span(a, pl, p / pl.nqb, p % pl.nqb, sp, nt);
+      if (r < at + n) {
+        bars.plan[0] = p / pl.nqb;
+        bars.plan[1] = p % pl.nqb;
+        bars.plan[2] = (int)(r - at);
+        break;
+      }
+      at += n;
+    }
+  }
+  if (threadIdx.x == 0 && *err != 0) bars.abort = 1;   // an earlier call failed: every output shows it
+  __syncthreads();
+  const uint32_t tmem = bars.tmem_base;
+  TcIter c;
+  c.b = idle ? 0 : bars.plan[0];
+  c.qb = idle ? 0 : bars.plan[1];
+  c.kvh = idle ? 0 : (int)(lo / S);
+  c.j0 = idle ? 0 : bars.plan[2];
+  c.left = hi - lo;
+  if (threadIdx.x == 0) {
+    TcPiece pc = {};
+    TcIter c2 = c;
+    TcItem it;
+    if (next_item(a, pl, c2, it)) pc = {it.b, it.qb, it.kvh, it.j0, it.j1, it.n, 1, 0};
+    pieces[blockIdx.x] = pc;
+  }
+  float* my_scratch = scratch + (size_t)blockIdx.x * kTile * (kPgD + 4);
+  const int rb = paged_row_bytes(FP8, a.Hkv);
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    softmax_role<FP8>(warp >> 2, a, pl, c, bars, abort_flag, err, part_o, part_ml, my_scratch, tmem);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+      // ---------------------------------------------------- K and V loads
+      uint32_t seq = 0, issued[2] = {0, 0};
+      const int page_rows = 1 << a.page_shift, piece = min(kTile, page_rows);
+      const int pieces_per_tile = kTile / piece;
+      const uint32_t piece_bytes = (uint32_t)piece * 128u;   // of one half (bf16) or of all codes
+      TcItem it;
+      bool ok = true;
+      while (ok && next_item(a, pl, c, it)) {
+        const int32_t* trow = a.table + (long long)it.b * a.max_pages;
+        const int e_last = it.top > 0 ? (it.top - 1) >> a.page_shift : 0;
+        int e0 = it.j0 * kTile >> a.page_shift;
+        int pg = e0 + lane <= e_last ? __ldg(trow + e0 + lane) : 0;
+        int pg_next = e0 + 32 + lane <= e_last ? __ldg(trow + e0 + 32 + lane) : 0;
+        for (int j = it.j0; j < it.j1 && ok; ++j, ++seq) {
+          const int first = j * kTile >> a.page_shift;
+          if (first >= e0 + 32) {
+            e0 += 32;
+            pg = pg_next;
+            pg_next = e0 + 32 + lane <= e_last ? __ldg(trow + e0 + 32 + lane) : 0;
+          }
+          // lane: piece (lane / 2) % 16 of the tile, half lane % 2
+          const int pi = lane >> 1, half = lane & 1;
+          const int page = __shfl_sync(0xffffffffu, pg, (first - e0 + pi) & 31);
+          // pieces past the last key any token sees are not read
+          const int live = min(pieces_per_tile, max(0, (it.top - j * kTile + piece - 1) / piece));
+          const bool on = pi < live && (!FP8 || half == 0);
+          const int y = on ? (checked_page(page, a.num_pages, a.dbg) << a.page_shift) +
+                                 (j * kTile + pi * piece & (page_rows - 1))
+                           : 0;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            uint64_t* full = FP8 ? (kv ? &bars.rv_full : &bars.rk_full)
+                                 : (kv ? &bars.v_full[seq % kStages] : &bars.k_full[seq % kStages]);
+            uint64_t* empty = FP8 ? (kv ? &bars.rv_empty : &bars.rk_empty)
+                                  : (kv ? &bars.v_empty[seq % kStages] : &bars.k_empty[seq % kStages]);
+            const uint32_t use = FP8 ? seq : seq / kStages;
+            if (use > 0 && !warp_wait(empty, (use - 1) & 1u, abort_flag, err, 31)) {
+              ok = false;
+              break;
+            }
+            unsigned char* dst = FP8 ? sRaw + kv * kRawBytes + pi * piece_bytes
+                                     : (kv ? sV : sK) + (seq % kStages) * kTileBytes + half * kHalfBytes +
+                                           pi * piece_bytes;
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * piece_bytes * (FP8 ? 1u : 2u));
+            __syncwarp();
+            if (on) tma_load_2d(dst, kv ? &map_v : &map_k, full, it.kvh * kPgD + (FP8 ? 0 : half * 64), y);
+            issued[kv] = seq + 1;
+          }
+        }
+      }
+      if (!ok || *abort_flag) {   // after an abort: copies in flight land before the CTA exits
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+          for (uint32_t i = issued[kv] > kStages ? issued[kv] - kStages : 0; i < issued[kv]; ++i) {
+            // E4M3 has one raw tile per cache, bf16 a tile per stage
+            if (FP8 && i + 1 < issued[kv]) continue;
+            uint64_t* full = FP8 ? (kv ? &bars.rv_full : &bars.rk_full)
+                                 : (kv ? &bars.v_full[i % kStages] : &bars.k_full[i % kStages]);
+            if (!mbar_wait_drain(full, (FP8 ? i : i / kStages) & 1u) && err) atomicCAS(err, 0, 44);
+          }
+      }
+    } else if (warp == 9) {
+      if (lane == 0) mma_role(a, pl, c, bars, abort_flag, err, sQ, sK, sV, tmem, FP8);
+      __syncwarp();
+    } else if (warp == 10) {
+      // ------------------------------------------------------------ Q loads
+      if (lane == 0) {
+        uint32_t nq[2] = {0, 0};
+        const uint32_t bytes = (uint32_t)(pl.tpt * a.G) * 256u;
+        TcItem it;
+        bool ok = true;
+        while (ok && next_item(a, pl, c, it)) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || (x == 0 ? it.cntA == 0 : it.split)) continue;
+            if (nq[x] > 0 && !mbar_wait(&bars.q_empty[x], (nq[x] - 1) & 1u, abort_flag, err, 32)) {
+              ok = false;
+              continue;
+            }
+            ++nq[x];
+            mbar_arrive_expect_tx(&bars.q_full[x], bytes);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(sQ + x * kTileBytes + h * kHalfBytes, &map_q, &bars.q_full[x], h * 64, it.kvh * a.G,
+                          it.tok0 + x * pl.tpt);
+          }
+        }
+        if (!ok || *abort_flag)
+          for (int x = 0; x < 2; ++x)
+            if (nq[x] > 0 && !mbar_wait_drain(&bars.q_full[x], (nq[x] - 1) & 1u) && err) atomicCAS(err, 0, 45);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    // ------------------------------ V cleaning; E4M3: codes to bf16 operands
+    const int t = threadIdx.x & 127;   // row of the tile
+    const uint32_t sw = (uint32_t)(t & 7);
+    uint32_t seq = 0, items = 0;
+    TcItem it;
+    bool ok = true;
+    for (; next_item(a, pl, c, it); ++items) {   // (after an abort too: the barrier below takes all four warps)
+      uint32_t(*bad)[4] = bars.bad[items % kBadRing];
+      if (t < kBadTiles * 4) bad[t >> 2][t & 3] = 0u;
+      named_sync(3, 128);
+      const int first_masked = it.first_masked();
+      for (int j = it.j0; j < it.j1 && ok; ++j, ++seq) {
+        const uint32_t s = seq % kStages, ph = (seq / kStages) & 1u;
+        const int key = j * kTile + t;
+        const bool masked = j >= first_masked;
+        unsigned char* vrow = sV + s * kTileBytes + (uint32_t)t * 128u;
+        bool flag = false;
+        if constexpr (!FP8) {
+          ok = warp_wait(&bars.v_full[s], ph, abort_flag, err, 33);
+          if (!ok) break;
+          if (masked) {
+            if (key >= it.top) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                *reinterpret_cast<uint4*>(vrow + (e >> 3) * kHalfBytes + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            } else if (key > it.pos0) {
+#pragma unroll 4
+              for (int e = 0; e < 16; ++e) {
+                uint4* p = reinterpret_cast<uint4*>(vrow + (e >> 3) * kHalfBytes + (((uint32_t)e & 7u) ^ sw) * 16);
+                uint4 v = *p;
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                bool hit = false;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  if ((w[u] & 0x7f80u) == 0x7f80u) w[u] &= 0xffff0000u, hit = true;
+                  if ((w[u] & 0x7f800000u) == 0x7f800000u) w[u] &= 0x0000ffffu, hit = true;
+                }
+                if (hit) {
+                  *p = make_uint4(w[0], w[1], w[2], w[3]);
+                  flag = true;
+                }
+              }
+            }
+            if (flag) atomicOr(&bad[j - first_masked][t >> 5], 1u << (t & 31));
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.v_clean[s]);
+          }
+        } else {
+          const bool seen = key < it.top;
+          uint32_t sck = 0u, scv = 0u;
+          if (seen) {
+            const long long off =
+                row_offset(a.table + (long long)it.b * a.max_pages, key, a.page_shift, a.num_pages, rb, a.dbg);
+            sck = __ldg(a.kp + off + a.Hkv * kPgD + it.kvh);
+            scv = __ldg(a.vp + off + a.Hkv * kPgD + it.kvh);
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = ok && warp_wait(kv ? &bars.rv_full : &bars.rk_full, seq & 1u, abort_flag, err, 42);
+            if (!ok) break;
+            const unsigned char* raw = sRaw + kv * kRawBytes + (uint32_t)t * 128u;
+            uint4 cd[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              cd[e] = *reinterpret_cast<const uint4*>(raw + (((uint32_t)e ^ sw) * 16));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kv ? &bars.rv_empty : &bars.rk_empty);
+            if (seq >= kStages)
+              ok = warp_wait(kv ? &bars.v_empty[s] : &bars.k_empty[s], ph ^ 1u, abort_flag, err, 43);
+            if (!ok) break;
+            const float sc = e8m0_value(kv ? scv : sck);
+            const bool partial = kv && masked && key > it.pos0;   // some token does not see this row
+            unsigned char* drow = (kv ? sV : sK) + s * kTileBytes + (uint32_t)t * 128u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {   // 16 codes -> two 16-byte chunks of bf16
+              const uint32_t w[4] = {cd[e].x, cd[e].y, cd[e].z, cd[e].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                o[2 * u] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[u] & 0xffffu), sc);
+                o[2 * u + 1] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[u] >> 16), sc);
+              }
+              if (kv && partial) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                  if ((o[u] & 0x7f80u) == 0x7f80u) o[u] &= 0xffff0000u, flag = true;
+                  if ((o[u] & 0x7f800000u) == 0x7f800000u) o[u] &= 0x0000ffffu, flag = true;
+                }
+              }
+              if (kv && !seen) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) o[u] = 0u;
+              }
+              unsigned char* d = drow + (e >> 2) * kHalfBytes;
+              const uint32_t c0 = (uint32_t)(2 * e) & 7u;
+              *reinterpret_cast<uint4*>(d + ((c0 ^ sw) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(d + (((c0 + 1) ^ sw) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            if (kv && flag && seen) atomicOr(&bad[j - first_masked][t >> 5], 1u << (t & 31));
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kv ? &bars.v_full[s] : &bars.k_full[s]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of items that several CTAs share.  Block (c, g): the item
+// that CTA c is the first to continue; rows g * 32 .. + 31, a warp per row.
+__global__ void __launch_bounds__(256)
+paged_tc_merge_kernel(const PagedArgs a, const TcPlan pl, const TcPiece* __restrict__ pieces,
+                      const float* __restrict__ part_o, const float* __restrict__ part_ml,
+                      const int* __restrict__ err) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = blockIdx.x + 1;
+  const TcPiece me = pieces[c], prev = pieces[c - 1];
+  if (!me.valid || me.j0 == 0) return;
+  auto same = [&](const TcPiece& o) { return o.valid && o.b == me.b && o.qb == me.qb && o.kvh == me.kvh; };
+  if (same(prev) && prev.j0 > 0) return;   // not the first to continue it
+  int last = c;                            // the piece that ends the item
+  for (int end = me.j1; end < me.n;) {
+    ++last;
+    if (last >= pl.W) return;              // (never: the pieces cover the item)
+    end = pieces[last].j1;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int C = last - c + 2;
+  // contributor i: the beginning (slot 1 of CTA c - 1), then slot 0 of CTAs c ..
+  auto slot = [&](int i) { return i == 0 ? 2ll * (c - 1) + 1 : 2ll * (c - 1 + i); };
+  const bool failed = *err != 0;
+  SeqSpan s;
+  int nt;
+  item_span(a, pl, me.b, me.qb, s, nt);
+  for (int q = 0; q < 4; ++q) {
+    const int row = blockIdx.y * 32 + q * 8 + warp;
+    const int x = row >> 7, rr = row & 127, tr = rr / a.G;
+    const int t = x * pl.tpt + tr;
+    if (rr >= pl.tpt * a.G || t >= nt) continue;
+    float M = -INFINITY;
+    for (int i = lane; i < C; i += 32) M = fmaxf(M, __ldcg(part_ml + (slot(i) * 2 * kTile + row) * 2));
+    M = warp_max(M);
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < C; ++i) {
+      const long long at = slot(i) * 2 * kTile + row;
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml + at * 2));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part_o + at * kPgD) + lane);
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;
+      const float w = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);   // (a NaN sum counts)
+      if (w == 0.f) continue;
+      L = fmaf(ml.y, w, L);
+      o.x = fmaf(v.x, w, o.x);
+      o.y = fmaf(v.y, w, o.y);
+      o.z = fmaf(v.z, w, o.z);
+      o.w = fmaf(v.w, w, o.w);
+    }
+    const bool none = L == 0.f;
+    const float inv = failed ? __uint_as_float(0x7fc00000u) : (none ? 0.f : 1.f / L);
+    const long long at = (long long)(s.begin + me.qb * pl.tpi + t) * a.Hq + me.kvh * a.G + rr % a.G;
+    reinterpret_cast<uint2*>(a.out + at * kPgD)[lane] =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (lane == 0 && a.lse != nullptr)
+      a.lse[at] = failed ? __uint_as_float(0x7fc00000u) : (none ? -INFINITY : (M + log2f(L)) * kPgLn2);
+  }
+}
+
+TcPlan tc_plan(int B, int G, int max_q) {
+  TcPlan pl;
+  pl.tpt = kTile / G;
+  pl.tpi = 2 * pl.tpt;
+  pl.nqb = (max_q + pl.tpi - 1) / pl.tpi;
+  pl.P = B * pl.nqb;
+  pl.W = device_sm_count();
+  return pl;
+}
+
+constexpr size_t kTcHead = 256;   // the kernel error word
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+size_t tc_part_o_bytes(const TcPlan& pl) { return (size_t)pl.W * 2 * 2 * kTile * kPgD * 4; }
+size_t tc_part_ml_bytes(const TcPlan& pl) { return (size_t)pl.W * 2 * 2 * kTile * 2 * 4; }
+size_t tc_scratch_bytes(const TcPlan& pl) { return (size_t)pl.W * kTile * (kPgD + 4) * 4; }
+size_t tc_pieces_bytes(const TcPlan& pl) { return up256(pl.W * sizeof(TcPiece)); }
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+// q [N][Hq][128]: box of 64 elements x G heads x tpt tokens.
+bool make_q_map(CUtensorMap* m, const PagedArgs& a, int tpt) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kPgD, (cuuint64_t)a.Hq, (cuuint64_t)a.N};
+  cuuint64_t strides[2] = {(cuuint64_t)kPgD * 2, (cuuint64_t)a.q_stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)tpt};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A pool as [rows][row elements]: box of 128 bytes x a page (at most a tile).
+bool make_pool_map(CUtensorMap* m, const PagedArgs& a, const uint8_t* pool, bool fp8) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int rb = paged_row_bytes(fp8, a.Hkv), rows = 1 << a.page_shift;
+  cuuint64_t dims[2] = {(cuuint64_t)(fp8 ? rb : rb / 2), (cuuint64_t)a.num_pages << a.page_shift};
+  cuuint64_t strides[1] = {(cuuint64_t)rb};
+  cuuint32_t box[2] = {fp8 ? 128u : 64u, (cuuint32_t)(rows < kTile ? rows : kTile)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(pool),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8>
+cudaError_t launch_tc(const PagedArgs& a, void* ws, cudaStream_t st) {
+  const TcPlan pl = tc_plan(a.B, a.G, a.max_q);
+  CUtensorMap mq, mk, mv;
+  if (!make_q_map(&mq, a, pl.tpt) || !make_pool_map(&mk, a, a.kp, FP8) || !make_pool_map(&mv, a, a.vp, FP8))
+    return cudaErrorInvalidValue;
+  char* p = static_cast<char*>(ws);
+  int* err = reinterpret_cast<int*>(p);
+  p += kTcHead;
+  TcPiece* pieces = reinterpret_cast<TcPiece*>(p);
+  p += tc_pieces_bytes(pl);
+  float* po = reinterpret_cast<float*>(p);
+  p += tc_part_o_bytes(pl);
+  float* pml = reinterpret_cast<float*>(p);
+  p += tc_part_ml_bytes(pl);
+  float* scratch = reinterpret_cast<float*>(p);
+  auto kern = paged_attn_tc_kernel<FP8>;
+  cudaError_t e = ensure_dynamic_smem((const void*)kern, tc_smem<FP8>());
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3((unsigned)pl.W), dim3(kTcThreads), tc_smem<FP8>(), st, mq, mk, mv, a, pl, pieces, po, pml,
+                 scratch, err);
+  if (e != cudaSuccess) return e;
+  if (pl.W > 1) {
+    e = launch_pdl(paged_tc_merge_kernel, dim3((unsigned)(pl.W - 1), 2 * kTile / 32), dim3(256), 0, st, a, pl, pieces,
+                   po, pml, err);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t paged_tc_workspace_bytes(int B, int G, int max_q) {
+  const TcPlan pl = tc_plan(B, G, max_q);
+  return kTcHead + tc_pieces_bytes(pl) + tc_part_o_bytes(pl) + tc_part_ml_bytes(pl) + up256(tc_scratch_bytes(pl));
+}
+
+cudaError_t launch_paged_tc(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {
+  return fp8 ? launch_tc<true>(a, ws, st) : launch_tc<false>(a, ws, st);
+}
+
+}  // namespace sa
