@@ -832,8 +832,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               cd[e] = *reinterpret_cast<const uint4*>(raw + (((uint32_t)e ^ sw) * 16));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(kv ? &bars.rv_empty : &bars.rk_empty);
             if (seq >= kStages)
               ok = warp_wait(kv ? &bars.v_empty[s] : &bars.k_empty[s], ph ^ 1u, abort_flag, err, 43);
             if (!ok) break;
@@ -868,7 +866,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (kv && flag && seen) atomicOr(&bad[j - first_masked][t >> 5], 1u << (t & 31));
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(kv ? &bars.v_full[s] : &bars.k_full[s]);
+            // the raw tile is given back only here, when what was read of it has
+            // been used: given back right behind the loads, rows of the next
+            // tile were seen in it
+            if (lane == 0) {
+              mbar_arrive(kv ? &bars.v_full[s] : &bars.k_full[s]);
+              mbar_arrive(kv ? &bars.rv_empty : &bars.rk_empty);
+            }
           }
         }
       }

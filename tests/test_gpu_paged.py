@@ -403,6 +403,38 @@ def test_sparse_decode(kv_type, hkv, G, k):
     _check_attn(got, lse, P.paged_sparse_attention(q, *pools, table, idx, count, kv_type), k)
 
 
+@pytest.mark.parametrize("kv_type", TYPES)
+def test_a_long_chunk_is_the_same_every_time(kv_type):
+    """Many items per SM, thousands of key tiles: every run gives the same bits,
+    and the log-sum-exp is that of fp32 products (error: 130 * 2^-24 * the sum
+    of magnitudes, below 60 for these inputs, twice; and the sums')."""
+    hkv, G, page, T, S = 8, 4, 64, 1536, 12000
+    g = torch.Generator(device=dev()).manual_seed(3)
+    num_pages = -(-S // page)
+    pools = sa.sa_paged_kv_alloc(num_pages, page, hkv, kv_type, device=dev())
+    k, v = (torch.randn(S, hkv, 128, device=dev(), generator=g).bfloat16() for _ in range(2))
+    table = torch.randperm(num_pages, device=dev(), generator=g).int()[None]
+    sa.sa_paged_kv_write(k, v, *pools, table, i32([0, S]), i32([S]))
+    rows = sa.sa_paged_kv_gather(*pools, table, torch.arange(S, device=dev(), dtype=torch.int32)[None], i32([S]))
+    kr, vr = (r[0, :, :hkv * 128].float().view(S, hkv, 128).transpose(0, 1) for r in rows)
+    q = torch.randn(T, hkv * G, 128, device=dev(), generator=g).bfloat16()
+    args = (q, *pools, table, i32([0, T]), i32([S]), T)
+    out, lse = sa.sa_paged_attn(*args, with_lse=True)
+    for _ in range(8):
+        o2, l2 = sa.sa_paged_attn(*args, with_lse=True)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    seen = torch.arange(S, device=dev()) <= (S - T + torch.arange(T, device=dev()))[:, None]
+    for h in range(hkv):
+        z = torch.matmul(q[:, h * G:h * G + G].float().transpose(0, 1), kr[h].T) * 128 ** -0.5
+        z.masked_fill_(~seen, float("-inf"))
+        ref = torch.logsumexp(z, -1)
+        assert (lse[:, h * G:h * G + G].T - ref).abs().max() < 2 * 130 * 2.0 ** -24 * 60 + 2.0 ** -15
+        p = torch.exp(z - ref[..., None])
+        o, mag = torch.matmul(p, vr[h]), torch.matmul(p, vr[h].abs())
+        err = (out[:, h * G:h * G + G].transpose(0, 1).float() - o).abs()
+        assert (err <= 2.0 ** -8 * (mag + o.abs()) * 1.01 + 2.0 ** -10 * mag).all()
+
+
 # ---------------------------------------------------------- in use together
 
 @pytest.mark.parametrize("kv_type", TYPES)
