@@ -51,7 +51,7 @@ constexpr uint32_t kHalfBytes = kTile * 128;    // 64 elements of 128 rows
 constexpr uint32_t kTileBytes = 2 * kHalfBytes; // 128 x 128 bf16
 constexpr int kStages = 2;
 constexpr uint32_t kRawBytes = kTile * 128;     // 128 rows of codes
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;   // 2 * 184 + 2 * 72 = 4 * 128 per warpgroup at launch
+constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;   // 2 * 152 + 2 * 104 = 4 * 128 per warpgroup at launch
 constexpr int kBadRing = 8;                     // items whose bad-row masks are kept
 constexpr int kBadTiles = 3;                    // key tiles a token of an item may not see in full
 
@@ -185,20 +185,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Descriptor of an operand whose reduction index runs over rows of 128
-// swizzled bytes (64 elements of the other index): 8-row groups 1024 bytes
-// apart, the next 64 elements kHalfBytes apart.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
-  d |= (uint64_t)(kHalfBytes >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -221,6 +216,37 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
+}
+
+// Waits for this thread's TMEM loads; ties the 32 registers a load fills to
+// the wait, so that nothing reads them before it.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+      :
+      : "memory");
+}
+
+// Largest of 32 scores, those beyond column `last` left out.
+__device__ __forceinline__ float max32(const uint32_t* s, int last) {
+  float v[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(s[e]);
+  if (last < 31) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = e <= last ? v[e] : -INFINITY;
+  }
+  float m[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) m[q] = fmaxf(v[q], v[q + 4]);
+#pragma unroll
+  for (int e = 8; e < 32; e += 8)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m[q] = fmaxf(fmaxf(m[q], v[e + q]), v[e + q + 4]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -296,25 +322,20 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
       ++ns;
       if (ok && any) {
         tc_fence_after();
-        float s[kTile];
+        // scores are read twice, 32 columns at a time: for the maximum, then
+        // for the exponentials (a row of 128 would not stay in registers)
+        const int last = kb + kTile - 1 > wmin ? limit - kb : kTile;   // columns beyond it are masked
+        float mx = -INFINITY;
+        {
+          uint32_t s[2][32];
+          tmem_ld32(tS, s[0]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, reinterpret_cast<uint32_t*>(s) + 32 * q);
-        tmem_ld_wait();
-        if (kb + kTile - 1 > wmin) {
-          const int last = limit - kb;
-#pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] = e <= last ? s[e] : -INFINITY;
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait32(s[q & 1]);
+            if (q < 3) tmem_ld32(tS + 32 * (q + 1), s[(q + 1) & 1]);
+            mx = fmaxf(mx, max32(s[q & 1], last - 32 * q));
+          }
         }
-        float m4[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) m4[q] = fmaxf(fmaxf(s[q], s[q + 4]), s[q + 8]);
-#pragma unroll
-        for (int e = 12; e < kTile - 4; e += 8)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) m4[q] = fmaxf(fmaxf(m4[q], s[e + q]), s[e + 4 + q]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], s[kTile - 4 + q]);
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         const bool up = mx > m + lazy;
         if (i > 0 && __any_sync(0xffffffffu, up)) {
           const float f = up ? ex2((m - mx) * qs) : 1.f;   // 0 when nothing was seen before
@@ -323,7 +344,7 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
           for (int q = 0; q < 4; ++q) {
             uint32_t o[32];
             tmem_ld32(tO + 32 * q, o);
-            tmem_ld_wait();
+            tmem_ld_wait32(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             tmem_st32(tO + 32 * q, o);
@@ -332,19 +353,30 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
         if (up) m = mx;
         const float nm = m == -INFINITY ? 0.f : -m * qs;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        {
+          uint32_t s[2][32];
+          tmem_ld32(tS, s[0]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait32(s[q & 1]);
+            if (q < 3) tmem_ld32(tS + 32 * (q + 1), s[(q + 1) & 1]);
+            uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float2 v = fma2(make_float2(s[64 * h + 2 * e], s[64 * h + 2 * e + 1]), make_float2(qs, qs),
-                            make_float2(nm, nm));
-            v.x = ex2(v.x);
-            v.y = ex2(v.y);
-            sum[e & 1] = add2(sum[e & 1], v);
-            p[e] = pack_bf16x2(v.x, v.y);
+            for (int e = 0; e < 16; ++e) {
+              float2 v = make_float2(__uint_as_float(s[q & 1][2 * e]), __uint_as_float(s[q & 1][2 * e + 1]));
+              if (last < kTile) {
+                v.x = 32 * q + 2 * e <= last ? v.x : -INFINITY;
+                v.y = 32 * q + 2 * e + 1 <= last ? v.y : -INFINITY;
+              }
+              v = fma2(v, make_float2(qs, qs), make_float2(nm, nm));
+              v.x = ex2(v.x);
+              v.y = ex2(v.y);
+              sum[e & 1] = add2(sum[e & 1], v);
+              p[e] = pack_bf16x2(v.x, v.y);
+            }
+            // P over the scores: these 16 columns were read before
+            tmem_st16(tS + 16 * q, p);
           }
-          tmem_st32(tS + 32 * h, p);
         }
         sum[0] = add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
@@ -370,7 +402,7 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
           for (int q = 0; q < 4; ++q) {
             uint32_t o[32];
             tmem_ld32(tO + 32 * q, o);
-            tmem_ld_wait();
+            tmem_ld_wait32(o);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               reinterpret_cast<uint4*>(dst + 32 * q)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -411,7 +443,7 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
       for (int q = 0; q < 4; ++q) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * q, o);
-        tmem_ld_wait();
+        tmem_ld_wait32(o);
         if (rowok) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
@@ -471,27 +503,62 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
 
 // --------------------------------------------------------------------- MMA
 
+// Operand descriptors (128-byte swizzle, 8-row groups 1024 bytes apart): low
+// words hold the start address in 16-byte units and a constant offset, high
+// words are constant.  Q and K run along the reduction index in a row; V's
+// reduction index runs over the rows, its next 64 columns are kHalfBytes on.
+constexpr uint32_t kDescLoK = (16u >> 4) << 16;
+constexpr uint32_t kDescLoV = (kHalfBytes >> 4) << 16;
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+
+// True in one lane of the warp, which issues the warp's tcgen05 operations:
+// the same lane every time, known to the compiler as a single one, so the
+// operands stay in uniform registers (an ordinary lane test made every issue
+// ten times as long).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// The whole warp walks the items and waits; one lane issues.
 __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, TcIter c, TcBars& bars,
                                          volatile int* abort_flag, int* err, unsigned char* sQ, unsigned char* sK,
                                          unsigned char* sV, uint32_t tmem, const bool fp8) {
   constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kTile);
   constexpr uint32_t kIdO = kIdS | (1u << 16);   // V: the reduction index is the row
+  const uint32_t q_lo = uniform(kDescLoK | (smem_u32(sQ) >> 4)), k_lo = uniform(kDescLoK | (smem_u32(sK) >> 4)),
+                 v_lo = uniform(kDescLoV | (smem_u32(sV) >> 4));
+  tmem = uniform(tmem);
   uint32_t seq0 = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean = 0u;
   TcItem it;
   bool ok = true;
+  // scores of tile x against its i-th key tile
   auto qk = [&](int x, int i) -> bool {
     const uint32_t seq = seq0 + (uint32_t)(it.tile_of(x, i) - it.j0);
-    const uint32_t s = seq % kStages;
-    if (!mbar_wait(&bars.k_full[s], (seq / kStages) & 1u, abort_flag, err, 36)) return false;
+    const uint32_t s = uniform(seq % kStages);
+    if (!warp_wait(&bars.k_full[s], (seq / kStages) & 1u, abort_flag, err, 36)) return false;
     tc_fence_after();
-    const uint32_t qa = smem_u32(sQ) + (x && !it.split ? kTileBytes : 0u), ka = smem_u32(sK) + s * kTileBytes;
+    const uint32_t ql = uniform(q_lo + (x && !it.split ? kTileBytes >> 4 : 0u)), kl = k_lo + s * (kTileBytes >> 4);
+    const bool release = x || it.split;
+    if (elect_lane()) {
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const uint32_t off = (uint32_t)(ks >> 2) * kHalfBytes + (uint32_t)(ks & 3) * 32u;
-      umma_bf16(tmem + x * kTile, sdesc_k_sw128(qa + off), sdesc_k_sw128(ka + off), kIdS, ks > 0);
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t off = (((uint32_t)ks >> 2) * kHalfBytes + ((uint32_t)ks & 3u) * 32u) >> 4;
+        umma_bf16(tmem + x * kTile, desc_of(ql + off), desc_of(kl + off), kIdS, ks > 0);
+      }
+      umma_commit(&bars.s_full[x]);
+      if (release) umma_commit(&bars.k_empty[s]);
     }
-    umma_commit(&bars.s_full[x]);
-    if (x || it.split) umma_commit(&bars.k_empty[s]);
+    __syncwarp();
     return true;
   };
   while (ok && next_item(a, pl, c, it)) {
@@ -499,11 +566,11 @@ __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, T
     const int most = max(cnt[0], cnt[1]);
     const int first_masked = it.first_masked();
     if (cnt[0] > 0) {
-      if (!mbar_wait(&bars.q_full[0], nq[0] & 1u, abort_flag, err, 37)) break;
+      ok = warp_wait(&bars.q_full[0], nq[0] & 1u, abort_flag, err, 37);
       ++nq[0];
     }
-    if (!it.split) {
-      if (!mbar_wait(&bars.q_full[1], nq[1] & 1u, abort_flag, err, 37)) break;
+    if (ok && !it.split) {
+      ok = warp_wait(&bars.q_full[1], nq[1] & 1u, abort_flag, err, 37);
       ++nq[1];
     }
 #pragma unroll
@@ -514,44 +581,48 @@ __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, T
       for (int x = 0; x < 2; ++x) {
         if (i >= cnt[x] || !ok) continue;
         const int j = it.tile_of(x, i);
-        const uint32_t seq = seq0 + (uint32_t)(j - it.j0), s = seq % kStages;
-        ok = mbar_wait(&bars.v_full[s], (seq / kStages) & 1u, abort_flag, err, 38);
+        const uint32_t seq = seq0 + (uint32_t)(j - it.j0), s = uniform(seq % kStages);
+        ok = warp_wait(&bars.v_full[s], (seq / kStages) & 1u, abort_flag, err, 38);
         if (ok && !fp8 && j >= first_masked) {
           // cleaned once per tile: A waits (its pair B needs no wait of its own
           // unless A has no such tile)
           const bool mine = it.split || x == 0 || i >= cnt[0];
           if (mine) {
-            ok = mbar_wait(&bars.v_clean[s], (clean >> s) & 1u, abort_flag, err, 39);
+            ok = warp_wait(&bars.v_clean[s], (clean >> s) & 1u, abort_flag, err, 39);
             clean ^= 1u << s;
           }
         }
-        ok = ok && mbar_wait(&bars.p_full[x], np[x] & 1u, abort_flag, err, 40);
+        ok = ok && warp_wait(&bars.p_full[x], np[x] & 1u, abort_flag, err, 40);
         if (!ok) break;
         ++np[x];
         tc_fence_after();
-        const uint32_t va = smem_u32(sV) + s * kTileBytes;
+        const uint32_t vl = v_lo + s * (kTileBytes >> 4);
+        const bool release = x || it.split, first = i == 0, end = i + 1 == cnt[x];
+        if (elect_lane()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          umma_bf16_ts(tmem + 2 * kTile + x * kTile, tmem + x * kTile + ks * 8, sdesc_mn_sw128(va + ks * 2048u), kIdO,
-                       i > 0 || ks > 0);
-        if (x || it.split) umma_commit(&bars.v_empty[s]);
-        if (i + 1 == cnt[x]) {
-          umma_commit(&bars.o_full[x]);
-        } else {
-          ok = qk(x, i + 1);
+          for (int ks = 0; ks < 8; ++ks)
+            umma_bf16_ts(tmem + 2 * kTile + x * kTile, tmem + x * kTile + ks * 8, desc_of(vl + ks * (2048u >> 4)), kIdO,
+                         !first || ks > 0);
+          if (release) umma_commit(&bars.v_empty[s]);
+          if (end) umma_commit(&bars.o_full[x]);
         }
+        __syncwarp();
+        if (!end) ok = qk(x, i + 1);
         // Q is free once its last scores are done
-        if (ok && !it.split && i + 2 == cnt[x]) umma_commit(&bars.q_empty[x]);
-        if (ok && !it.split && cnt[x] == 1) umma_commit(&bars.q_empty[x]);
-        if (ok && it.split && i + 1 == cnt[0] && x == 0) umma_commit(&bars.q_empty[0]);
+        const bool done_q = it.split ? x == 0 && end : i + 2 == cnt[x] || cnt[x] == 1;
+        if (ok && done_q && elect_lane()) umma_commit(&bars.q_empty[x]);
+        __syncwarp();
       }
     }
     seq0 += (uint32_t)(it.j1 - it.j0);
   }
   // (after an abort) everything issued is done before TMEM is freed
-  if (!ok || *abort_flag) {
-    umma_commit(&bars.drain);
-    if (!mbar_wait_drain(&bars.drain, 0) && err) atomicCAS(err, 0, 41);
+  if (__any_sync(0xffffffffu, !ok || *abort_flag != 0)) {
+    if (elect_lane()) {
+      umma_commit(&bars.drain);
+      if (!mbar_wait_drain(&bars.drain, 0) && err) atomicCAS(err, 0, 41);
+    }
+    __syncwarp();
   }
 }
 
@@ -733,8 +804,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           }
       }
     } else if (warp == 9) {
-      if (lane == 0) mma_role(a, pl, c, bars, abort_flag, err, sQ, sK, sV, tmem, FP8);
-      __syncwarp();
+      mma_role(a, pl, c, bars, abort_flag, err, sQ, sK, sV, tmem, FP8);
     } else if (warp == 10) {
       // ------------------------------------------------------------ Q loads
       if (lane == 0) {
