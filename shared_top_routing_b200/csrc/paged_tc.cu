@@ -185,14 +185,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -230,23 +222,37 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
       : "memory");
 }
 
-// Largest of 32 scores, those beyond column `last` left out.
-__device__ __forceinline__ float max32(const uint32_t* s, int last) {
-  float v[32];
+// A row of 128 scores in TMEM -> 2^(s qs + nm) as packed bf16, their sum and
+// the largest score; columns beyond `last` count as -inf when MASKED.
+template <bool MASKED>
+__device__ __forceinline__ void exp_tile(uint32_t tS, float qs, float nm, int last, uint32_t (&p)[64], float& mx,
+                                         float& sum) {
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t s[2][32];
+  tmem_ld32(tS, s[0]);
 #pragma unroll
-  for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(s[e]);
-  if (last < 31) {
+  for (int q = 0; q < 4; ++q) {
+    tmem_ld_wait32(s[q & 1]);
+    if (q < 3) tmem_ld32(tS + 32 * (q + 1), s[(q + 1) & 1]);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = e <= last ? v[e] : -INFINITY;
+    for (int e = 0; e < 16; ++e) {
+      float2 v = make_float2(__uint_as_float(s[q & 1][2 * e]), __uint_as_float(s[q & 1][2 * e + 1]));
+      if (MASKED) {
+        v.x = 32 * q + 2 * e <= last ? v.x : -INFINITY;
+        v.y = 32 * q + 2 * e + 1 <= last ? v.y : -INFINITY;
+      }
+      m4[e & 3] = fmaxf(fmaxf(m4[e & 3], v.x), v.y);
+      v = fma2(v, make_float2(qs, qs), make_float2(nm, nm));
+      v.x = ex2(v.x);
+      v.y = ex2(v.y);
+      acc[e & 1] = add2(acc[e & 1], v);
+      p[16 * q + e] = pack_bf16x2(v.x, v.y);
+    }
   }
-  float m[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) m[q] = fmaxf(v[q], v[q + 4]);
-#pragma unroll
-  for (int e = 8; e < 32; e += 8)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) m[q] = fmaxf(fmaxf(m[q], v[e + q]), v[e + q + 4]);
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  acc[0] = add2(acc[0], acc[1]);
+  sum = acc[0].x + acc[0].y;
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -322,64 +328,37 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
       ++ns;
       if (ok && any) {
         tc_fence_after();
-        // scores are read twice, 32 columns at a time: for the maximum, then
-        // for the exponentials (a row of 128 would not stay in registers)
-        const int last = kb + kTile - 1 > wmin ? limit - kb : kTile;   // columns beyond it are masked
-        float mx = -INFINITY;
-        {
-          uint32_t s[2][32];
-          tmem_ld32(tS, s[0]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_ld_wait32(s[q & 1]);
-            if (q < 3) tmem_ld32(tS + 32 * (q + 1), s[(q + 1) & 1]);
-            mx = fmaxf(mx, max32(s[q & 1], last - 32 * q));
-          }
-        }
-        const bool up = mx > m + lazy;
-        if (i > 0 && __any_sync(0xffffffffu, up)) {
+        // one pass with the maximum so far; only when the tile's own exceeds
+        // it by more than 2^8 (and for the first tile) a second pass
+        const int last = limit - kb;   // columns beyond it are masked
+        const bool masked = kb + kTile - 1 > wmin;
+        uint32_t p[64];
+        float sum;
+        while (true) {
+          const float nm = m == -INFINITY ? 0.f : -m * qs;
+          float mx;
+          if (masked) exp_tile<true>(tS, qs, nm, last, p, mx, sum);
+          else exp_tile<false>(tS, qs, nm, last, p, mx, sum);
+          const bool up = mx > m + lazy;
+          if (!__any_sync(0xffffffffu, up)) break;
           const float f = up ? ex2((m - mx) * qs) : 1.f;   // 0 when nothing was seen before
+          if (up) m = mx;
           l *= f;
+          if (i > 0) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32 * q, o);
-            tmem_ld_wait32(o);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * q, o);
+              tmem_ld_wait32(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(tO + 32 * q, o);
-          }
-        }
-        if (up) m = mx;
-        const float nm = m == -INFINITY ? 0.f : -m * qs;
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        {
-          uint32_t s[2][32];
-          tmem_ld32(tS, s[0]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_ld_wait32(s[q & 1]);
-            if (q < 3) tmem_ld32(tS + 32 * (q + 1), s[(q + 1) & 1]);
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 v = make_float2(__uint_as_float(s[q & 1][2 * e]), __uint_as_float(s[q & 1][2 * e + 1]));
-              if (last < kTile) {
-                v.x = 32 * q + 2 * e <= last ? v.x : -INFINITY;
-                v.y = 32 * q + 2 * e + 1 <= last ? v.y : -INFINITY;
-              }
-              v = fma2(v, make_float2(qs, qs), make_float2(nm, nm));
-              v.x = ex2(v.x);
-              v.y = ex2(v.y);
-              sum[e & 1] = add2(sum[e & 1], v);
-              p[e] = pack_bf16x2(v.x, v.y);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(tO + 32 * q, o);
             }
-            // P over the scores: these 16 columns were read before
-            tmem_st16(tS + 16 * q, p);
           }
         }
-        sum[0] = add2(sum[0], sum[1]);
-        l += sum[0].x + sum[0].y;
+        l += sum;
+        tmem_st32(tS, p);   // P over the scores
+        tmem_st32(tS + 32, p + 32);
         tmem_st_wait();
         tc_fence_before();
       }
@@ -513,10 +492,7 @@ constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
 
-// True in one lane of the warp, which issues the warp's tcgen05 operations:
-// the same lane every time, known to the compiler as a single one, so the
-// operands stay in uniform registers (an ordinary lane test made every issue
-// ten times as long).
+// True in one lane of the warp, the same one every time.
 __device__ __forceinline__ bool elect_lane() {
   uint32_t ok;
   asm volatile(
@@ -527,102 +503,95 @@ __device__ __forceinline__ bool elect_lane() {
   return ok != 0;
 }
 
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// The whole warp walks the items and waits; one lane issues.
+// One elected lane walks the items, waits and issues.  Waits cost a few hundred
+// clocks each on this path, during which the tensor core runs dry, so each
+// tile is waited for once (by the first of A and B that uses it) and before
+// the wait for P, and a product pair O += P V, S = Q K'^T is issued in one go.
 __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, TcIter c, TcBars& bars,
                                          volatile int* abort_flag, int* err, unsigned char* sQ, unsigned char* sK,
-                                         unsigned char* sV, uint32_t tmem, const bool fp8) {
+                                         unsigned char* sV, const uint32_t tmem, const bool fp8) {
   constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kTile);
   constexpr uint32_t kIdO = kIdS | (1u << 16);   // V: the reduction index is the row
-  const uint32_t q_lo = uniform(kDescLoK | (smem_u32(sQ) >> 4)), k_lo = uniform(kDescLoK | (smem_u32(sK) >> 4)),
-                 v_lo = uniform(kDescLoV | (smem_u32(sV) >> 4));
-  tmem = uniform(tmem);
+  const uint32_t q_lo = kDescLoK | (smem_u32(sQ) >> 4), k_lo = kDescLoK | (smem_u32(sK) >> 4),
+                 v_lo = kDescLoV | (smem_u32(sV) >> 4);
   uint32_t seq0 = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean = 0u;
+  uint32_t k_seen = 0, v_seen = 0;   // key tiles known to be in shared memory
   TcItem it;
   bool ok = true;
-  // scores of tile x against its i-th key tile
-  auto qk = [&](int x, int i) -> bool {
-    const uint32_t seq = seq0 + (uint32_t)(it.tile_of(x, i) - it.j0);
-    const uint32_t s = uniform(seq % kStages);
-    if (!warp_wait(&bars.k_full[s], (seq / kStages) & 1u, abort_flag, err, 36)) return false;
-    tc_fence_after();
-    const uint32_t ql = uniform(q_lo + (x && !it.split ? kTileBytes >> 4 : 0u)), kl = k_lo + s * (kTileBytes >> 4);
-    const bool release = x || it.split;
-    if (elect_lane()) {
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t off = (((uint32_t)ks >> 2) * kHalfBytes + ((uint32_t)ks & 3u) * 32u) >> 4;
-        umma_bf16(tmem + x * kTile, desc_of(ql + off), desc_of(kl + off), kIdS, ks > 0);
-      }
-      umma_commit(&bars.s_full[x]);
-      if (release) umma_commit(&bars.k_empty[s]);
+  auto seq_of = [&](int x, int i) { return seq0 + (uint32_t)(it.tile_of(x, i) - it.j0); };
+  auto need_k = [&](uint32_t seq) {
+    if (seq < k_seen) return;
+    ok = ok && mbar_wait(&bars.k_full[seq % kStages], (seq / kStages) & 1u, abort_flag, err, 36);
+    k_seen = seq + 1;
+  };
+  auto need_v = [&](uint32_t seq, bool masked) {
+    if (seq < v_seen) return;
+    const uint32_t s = seq % kStages;
+    ok = ok && mbar_wait(&bars.v_full[s], (seq / kStages) & 1u, abort_flag, err, 38);
+    if (!fp8 && masked) {   // cleaned first
+      ok = ok && mbar_wait(&bars.v_clean[s], (clean >> s) & 1u, abort_flag, err, 39);
+      clean ^= 1u << s;
     }
-    __syncwarp();
-    return true;
+    v_seen = seq + 1;
+  };
+  // scores of tile x against the key tile `seq`
+  auto qk = [&](int x, uint32_t seq) {
+    const uint32_t s = seq % kStages;
+    const uint32_t ql = q_lo + (x && !it.split ? kTileBytes >> 4 : 0u), kl = k_lo + s * (kTileBytes >> 4);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      const uint32_t off = (((uint32_t)ks >> 2) * kHalfBytes + ((uint32_t)ks & 3u) * 32u) >> 4;
+      umma_bf16(tmem + x * kTile, desc_of(ql + off), desc_of(kl + off), kIdS, ks > 0);
+    }
+    umma_commit(&bars.s_full[x]);
+    if (x || it.split) umma_commit(&bars.k_empty[s]);
   };
   while (ok && next_item(a, pl, c, it)) {
     const int cnt[2] = {it.cntA, it.cntB};
     const int most = max(cnt[0], cnt[1]);
     const int first_masked = it.first_masked();
-    if (cnt[0] > 0) {
-      ok = warp_wait(&bars.q_full[0], nq[0] & 1u, abort_flag, err, 37);
-      ++nq[0];
-    }
-    if (ok && !it.split) {
-      ok = warp_wait(&bars.q_full[1], nq[1] & 1u, abort_flag, err, 37);
-      ++nq[1];
-    }
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (ok && cnt[x] > 0) ok = qk(x, 0);
+    for (int x = 0; x < 2; ++x) {
+      if (cnt[x] == 0) continue;
+      if (x == 0 || !it.split) {
+        ok = ok && mbar_wait(&bars.q_full[x], nq[x] & 1u, abort_flag, err, 37);
+        ++nq[x];
+      }
+      need_k(seq_of(x, 0));
+      if (!ok) break;
+      tc_fence_after();
+      qk(x, seq_of(x, 0));
+    }
     for (int i = 0; i < most && ok; ++i) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (i >= cnt[x] || !ok) continue;
-        const int j = it.tile_of(x, i);
-        const uint32_t seq = seq0 + (uint32_t)(j - it.j0), s = uniform(seq % kStages);
-        ok = warp_wait(&bars.v_full[s], (seq / kStages) & 1u, abort_flag, err, 38);
-        if (ok && !fp8 && j >= first_masked) {
-          // cleaned once per tile: A waits (its pair B needs no wait of its own
-          // unless A has no such tile)
-          const bool mine = it.split || x == 0 || i >= cnt[0];
-          if (mine) {
-            ok = warp_wait(&bars.v_clean[s], (clean >> s) & 1u, abort_flag, err, 39);
-            clean ^= 1u << s;
-          }
-        }
-        ok = ok && warp_wait(&bars.p_full[x], np[x] & 1u, abort_flag, err, 40);
+        if (i >= cnt[x]) continue;
+        const uint32_t seq = seq_of(x, i), s = seq % kStages;
+        const bool end = i + 1 == cnt[x];
+        need_v(seq, it.tile_of(x, i) >= first_masked);
+        if (!end) need_k(seq_of(x, i + 1));
+        ok = ok && mbar_wait(&bars.p_full[x], np[x] & 1u, abort_flag, err, 40);
         if (!ok) break;
         ++np[x];
         tc_fence_after();
         const uint32_t vl = v_lo + s * (kTileBytes >> 4);
-        const bool release = x || it.split, first = i == 0, end = i + 1 == cnt[x];
-        if (elect_lane()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_bf16_ts(tmem + 2 * kTile + x * kTile, tmem + x * kTile + ks * 8, desc_of(vl + ks * (2048u >> 4)), kIdO,
-                         !first || ks > 0);
-          if (release) umma_commit(&bars.v_empty[s]);
-          if (end) umma_commit(&bars.o_full[x]);
-        }
-        __syncwarp();
-        if (!end) ok = qk(x, i + 1);
+        for (int ks = 0; ks < 8; ++ks)
+          umma_bf16_ts(tmem + 2 * kTile + x * kTile, tmem + x * kTile + ks * 8, desc_of(vl + ks * (2048u >> 4)), kIdO,
+                       i > 0 || ks > 0);
+        if (x || it.split) umma_commit(&bars.v_empty[s]);
+        if (!end) qk(x, seq_of(x, i + 1));
+        else umma_commit(&bars.o_full[x]);
         // Q is free once its last scores are done
-        const bool done_q = it.split ? x == 0 && end : i + 2 == cnt[x] || cnt[x] == 1;
-        if (ok && done_q && elect_lane()) umma_commit(&bars.q_empty[x]);
-        __syncwarp();
+        if (it.split ? x == 0 && end : i + 2 == cnt[x] || cnt[x] == 1) umma_commit(&bars.q_empty[x]);
       }
     }
     seq0 += (uint32_t)(it.j1 - it.j0);
   }
   // (after an abort) everything issued is done before TMEM is freed
-  if (__any_sync(0xffffffffu, !ok || *abort_flag != 0)) {
-    if (elect_lane()) {
-      umma_commit(&bars.drain);
-      if (!mbar_wait_drain(&bars.drain, 0) && err) atomicCAS(err, 0, 41);
-    }
-    __syncwarp();
+  if (!ok || *abort_flag) {
+    umma_commit(&bars.drain);
+    if (!mbar_wait_drain(&bars.drain, 0) && err) atomicCAS(err, 0, 41);
   }
 }
 
@@ -804,7 +773,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           }
       }
     } else if (warp == 9) {
-      mma_role(a, pl, c, bars, abort_flag, err, sQ, sK, sV, tmem, FP8);
+      if (elect_lane()) mma_role(a, pl, c, bars, abort_flag, err, sQ, sK, sV, tmem, FP8);
+      __syncwarp();
     } else if (warp == 10) {
       // ------------------------------------------------------------ Q loads
       if (lane == 0) {
