@@ -347,7 +347,8 @@ sa_status sa_paged_kv_gather(const void* k_pages, const void* v_pages, const int
  *         use; see the conventions above).  Its first int32 is the kernel
  *         error word: 0 after a good call, else the outputs hold NaN.
  * Supported: Hq % Hkv == 0; Hq/Hkv <= 16; N * Hq < 2^31. */
-size_t sa_paged_attn_workspace(int B, int N, int max_q, int Hq, int Hkv, int D, int kv_type);
+size_t sa_paged_attn_workspace(int B, int N, int max_q, int max_pages, int page_size, int Hq, int Hkv, int D,
+                               int kv_type);
 sa_status sa_paged_attn(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
                         const int32_t* block_table, const int32_t* q_start, const int32_t* kv_len, int B, int N,
                         int max_q, int max_pages, int num_pages, int page_size, int Hq, int Hkv, int D,

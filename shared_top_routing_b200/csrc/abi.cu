@@ -572,12 +572,14 @@ sa_status sa_paged_kv_gather(const void* k_pages, const void* v_pages, const int
   return ok();
 }
 
-size_t sa_paged_attn_workspace(int B, int N, int max_q, int Hq, int Hkv, int D, int kv_type) {
+size_t sa_paged_attn_workspace(int B, int N, int max_q, int max_pages, int page_size, int Hq, int Hkv, int D,
+                               int kv_type) {
   (void)D;
-  if (B <= 0 || N <= 0 || max_q <= 0 || Hkv <= 0 || Hkv > SA_PAGED_MAX_HKV || Hq < Hkv || Hq % Hkv != 0 ||
+  if (B <= 0 || N <= 0 || max_q <= 0 || max_pages <= 0 || page_size <= 0 || Hkv <= 0 || Hkv > SA_PAGED_MAX_HKV || Hq < Hkv || Hq % Hkv != 0 ||
       Hq / Hkv > 16)
     return 0;
-  return sa::paged_attn_workspace_bytes(kv_type == SA_KV_E4M3, B, N, max_q < N ? max_q : N, Hkv, Hq / Hkv) +
+  return sa::paged_attn_workspace_bytes(kv_type == SA_KV_E4M3, B, max_q < N ? max_q : N,
+                                        (long long)max_pages * page_size, Hkv, Hq / Hkv) +
          sa::kWsCanary;
 }
 
@@ -602,7 +604,7 @@ sa_status sa_paged_attn(const void* q, int64_t q_stride, const void* k_pages, co
   if (max_q > N) max_q = N;
   if ((long long)B * max_q > (1ll << 30))
     return fail(SA_ERR_UNSUPPORTED, "B*max_q=%lld too large", (long long)B * max_q);
-  const size_t need = sa_paged_attn_workspace(B, N, max_q, Hq, Hkv, D, kv_type);
+  const size_t need = sa_paged_attn_workspace(B, N, max_q, max_pages, page_size, Hq, Hkv, D, kv_type);
   if ((st = check_ws(ws, ws_bytes, need)) != SA_OK) return st;
   sa::PagedArgs a;
   a.q = static_cast<const uint16_t*>(q);

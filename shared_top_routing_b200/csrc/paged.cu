@@ -992,10 +992,9 @@ cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_
 // the cache once and is bound by HBM.  Longer chunks go to the tensor cores.
 static bool use_rows(int G, int max_q) { return max_q * G <= 16; }
 
-size_t paged_attn_workspace_bytes(int fp8, int B, int N, int max_q, int Hkv, int G) {
-  (void)N;
+size_t paged_attn_workspace_bytes(int fp8, int B, int max_q, long long capacity, int Hkv, int G) {
   return use_rows(G, max_q) ? paged_rows_workspace_bytes(fp8, B, Hkv, G, max_q)
-                            : paged_tc_workspace_bytes(B, G, max_q);
+                            : paged_tc_workspace_bytes(fp8, B, Hkv, G, max_q, capacity);
 }
 
 cudaError_t launch_paged_attn(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {

@@ -166,10 +166,10 @@ cudaError_t launch_paged_gather(const uint8_t* kp, const uint8_t* vp, const int3
 size_t paged_rows_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q);
 cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
 // Attention of many query rows per kv head on the tensor cores (paged_tc.cu).
-size_t paged_tc_workspace_bytes(int B, int G, int max_q);
+size_t paged_tc_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q, long long capacity);
 cudaError_t launch_paged_tc(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
 // Chunk attention: picks the kernel for the chunk's length.
-size_t paged_attn_workspace_bytes(int fp8, int B, int N, int max_q, int Hkv, int G);
+size_t paged_attn_workspace_bytes(int fp8, int B, int max_q, long long capacity, int Hkv, int G);
 cudaError_t launch_paged_attn(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
 
 }  // namespace sa

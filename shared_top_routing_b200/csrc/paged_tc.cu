@@ -2,33 +2,38 @@
 // (tcgen05, sm_100a): many query rows per kv head.
 //
 // Mathematics: out_t = sum_{j <= p_t} softmax_j(scale q_t.k_j) v_j, one pass
-// over the keys in tiles of 128 with a running maximum m and sum l per row:
+// over the keys in tiles of 128 with a reference m and a sum l per row:
 // S = Q K^T, P = 2^((S - m) c), l += sum P, O += P V (c = scale * log2 e);
-// when m rises, l and O are scaled by 2^((m_old - m) c).  O is scaled only
-// when the maximum rises by more than 2^8 (the sums stay far inside fp32 and
-// P, at most 2^8, keeps its relative precision in bf16).
+// when m rises, l and O are scaled by 2^((m_old - m) c).  m rises only when a
+// tile's maximum exceeds it by more than 8 / c (the sums stay far inside fp32
+// and P, at most 2^8, keeps its relative precision in bf16), so a tile takes
+// one pass and O is hardly ever scaled.
 //
 // Rows: the G query heads of a kv head times 128 / G tokens share a 128-row
 // tile (they read the same keys); an item is two such tiles, A and B, of one
-// sequence and kv head, with the key tiles up to its last token.  The two
-// tiles alternate: while one's scores go through the softmax, the tensor core
-// works for the other.  An item with tokens for one tile only lets A take its
-// even key tiles and B its odd ones, and joins them at the end.  The key
-// tiles of all items form one list, cut evenly over one CTA per SM (an item
-// cut in pieces is joined by paged_tc_merge_kernel), so ragged batches and
-// few long sequences load every SM alike.
+// sequence and kv head, with the key tiles up to its last token.  An item with
+// tokens for one tile only lets A take its even key tiles and B its odd ones,
+// and joins them at the end.  The key tiles of all items form one list, cut
+// evenly over one CTA per SM (an item cut in pieces is joined by
+// paged_tc_merge_kernel), so ragged batches and few long sequences load every
+// SM alike.  A and B alternate: while one's scores go through the softmax, the
+// tensor core works for the other.
 //
-// Bound: 4 * 128 flops per (row, key) on the tensor core, and the same number
-// of clocks for the exponentials (128 x 256 of them per key tile at 16 per
-// clock and SM, against 2048 clocks of MMA).
+// E4M3 caches are first written out in bf16 (exact) by paged_window_kernel, a
+// window of sequences or heads at a time, contiguous: a row is converted once
+// instead of once per query tile (codes converted beside the products:
+// 434 TFLOP/s).
 //
-// CTA of 512 threads, registers moved to the softmax warps (setmaxnreg):
+// Bound: 4 * 128 flops per (row, key) on the tensor core, and as many clocks
+// for the exponentials (128 x 256 of them per key tile at 16 per clock and SM,
+// against 2048 clocks of MMA).
+//
+// CTA of 512 threads:
 //   warps 0-3, 4-7   softmax of tile A, of tile B: one thread per row
 //   warp 8           K and V tiles by TMA, a page (or half of one) at a time
 //   warp 9           MMA issue; S and O in TMEM, P over S as the A operand
 //   warp 10          Q tiles by TMA
-//   warps 12-15      E4M3: codes to bf16 (exact) in the operand layout; both:
-//                    V rows no token of the item sees are zeroed, infinities
+//   warps 12-15      V rows no token of the item sees are zeroed, infinities
 //                    and NaN in rows only some see are taken out and added
 //                    to those rows' results at the end
 #include <cudaTypedefs.h>
@@ -50,21 +55,26 @@ constexpr int kTile = 128;                      // rows of a q tile, keys of a k
 constexpr uint32_t kHalfBytes = kTile * 128;    // 64 elements of 128 rows
 constexpr uint32_t kTileBytes = 2 * kHalfBytes; // 128 x 128 bf16
 constexpr int kStages = 2;
-constexpr uint32_t kRawBytes = kTile * 128;     // 128 rows of codes
 constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;   // 2 * 152 + 2 * 104 = 4 * 128 per warpgroup at launch
 constexpr int kBadRing = 8;                     // items whose bad-row masks are kept
 constexpr int kBadTiles = 3;                    // key tiles a token of an item may not see in full
+constexpr int kStageRow = 80;                   // bytes of a staged output row: 64 and a pad
 
+// Sequences [b0, b0 + nb) and kv heads [h0, h0 + nh) of a call; for E4M3 their
+// rows in bf16, [nb][cap][nh * 128] (K and V).
 struct TcPlan {
   int tpt, tpi, nqb, P;   // tokens per tile and item, items per sequence at most, items per kv head
   int W;                  // CTAs
+  int b0, nb, h0, nh;
+  long long cap;
+  const uint16_t* kw;
+  const uint16_t* vw;
 };
 
 struct TcBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_clean[kStages];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t rk_full, rk_empty, rv_full, rv_empty;   // E4M3: raw code tiles
   uint64_t drain;
   alignas(16) uint32_t bad[kBadRing][kBadTiles][4];   // V rows with infinities or NaN, by key (read 16 bytes a time)
   long long scan[kTcThreads / 32];
@@ -75,18 +85,16 @@ struct TcBars {
 static_assert(sizeof(TcBars) <= 1024 && offsetof(TcBars, bad) % 16 == 0 && offsetof(TcBars, scan) % 8 == 0,
               "barrier block");
 
-template <bool FP8>
-constexpr size_t tc_smem() {
-  return 1024 + 2 * kTileBytes + 2 * kStages * kTileBytes + (FP8 ? 2 * kRawBytes : 0) + 1024;
-}
+constexpr size_t kTcSmem = 1024 + 2 * kTileBytes + 2 * kStages * kTileBytes + 1024 + 8 * 32 * kStageRow;
+static_assert(kTcSmem <= 227 * 1024, "shared memory");
 
 // What a CTA's first piece is, for the merge.
 struct TcPiece {
   int b, qb, kvh, j0, j1, n, valid, pad;
 };
 
-// A piece of an item: sequence b, block qb of tpi tokens, kv head, key tiles
-// [j0, j1) of its n.
+// A piece of an item: sequence b, block qb of tpi tokens, kv head h0 + kvh,
+// key tiles [j0, j1) of its n.
 struct TcItem {
   int b, qb, kvh;
   int tok0, ntA, ntB;   // first token (packed), tokens of tile A and B
@@ -94,6 +102,7 @@ struct TcItem {
   int n, j0, j1;
   int cntA, cntB;       // key tiles of A and B
   bool split;           // B's rows are A's, over the odd key tiles
+  // the i-th key tile of A (x = 0) or B
   __device__ __forceinline__ int tile_of(int x, int i) const { return split ? j0 + 2 * i + x : j0 + i; }
   // first key tile that some token does not see in full
   __device__ __forceinline__ int first_masked() const { return pos0 < 0 ? 0 : (pos0 + 1) / kTile; }
@@ -108,22 +117,23 @@ __device__ __forceinline__ int item_span(const PagedArgs& a, const TcPlan& pl, i
   return max(1, (max(s.pos0 + t0 + nt, 0) + kTile - 1) / kTile);
 }
 
+// Where a CTA is in the list: sequence b0 + b.
 struct TcIter {
   int b, qb, kvh, j0;
   long long left;
 };
 
 __device__ __forceinline__ bool next_item(const PagedArgs& a, const TcPlan& pl, TcIter& c, TcItem& it) {
-  while (c.left > 0 && c.kvh < a.Hkv) {
+  while (c.left > 0 && c.kvh < pl.nh) {
     SeqSpan s;
     int nt;
-    const int n = item_span(a, pl, c.b, c.qb, s, nt);
+    const int n = item_span(a, pl, pl.b0 + c.b, c.qb, s, nt);
     if (n == 0) {
       c.qb = 0;
-      if (++c.b == a.B) c.b = 0, ++c.kvh;
+      if (++c.b == pl.nb) c.b = 0, ++c.kvh;
       continue;
     }
-    it.b = c.b, it.qb = c.qb, it.kvh = c.kvh;
+    it.b = pl.b0 + c.b, it.qb = c.qb, it.kvh = c.kvh;
     it.tok0 = s.begin + c.qb * pl.tpi;
     it.pos0 = s.pos0 + c.qb * pl.tpi;
     it.ntA = min(nt, pl.tpt);
@@ -146,7 +156,7 @@ __device__ __forceinline__ bool next_item(const PagedArgs& a, const TcPlan& pl, 
     c.j0 = 0;
     if (++c.qb == pl.nqb) {
       c.qb = 0;
-      if (++c.b == a.B) c.b = 0, ++c.kvh;
+      if (++c.b == pl.nb) c.b = 0, ++c.kvh;
     }
     return true;
   }
@@ -259,37 +269,15 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// A position's row in the pools: its offset in bytes.
-__device__ __forceinline__ long long row_offset(const int32_t* __restrict__ trow, int pos, int page_shift,
-                                                int num_pages, int rb, int* dbg) {
-  const int pg = checked_page(__ldg(trow + (pos >> page_shift)), num_pages, dbg);
-  return (((long long)pg << page_shift) + (pos & ((1 << page_shift) - 1))) * rb;
-}
-
-// Rare: adds the infinities and NaN of the flagged V rows a token sees to its
-// finished row (bf16) or partial row (fp32), whichever is given.
-template <bool FP8>
-__device__ __noinline__ void add_bad_rows(const uint8_t* __restrict__ vp, const int32_t* __restrict__ trow, int Hkv,
-                                          int kvh, int page_shift, int num_pages, int first_masked,
-                                          const uint32_t* bad, int limit, uint16_t* out, float* part) {
-  const int rb = paged_row_bytes(FP8, Hkv);
-  for (int i = 0; i < kBadTiles * kTile; ++i) {
-    const int key = first_masked * kTile + i;
-    if (key > limit) break;
-    if (!((bad[i >> 5] >> (i & 31)) & 1u)) continue;
-    const uint8_t* row = vp + row_offset(trow, key, page_shift, num_pages, rb, nullptr);
-    const bool whole = FP8 && row[Hkv * kPgD + kvh] == 255;   // the scale is NaN
-    for (int d = 0; d < kPgD; ++d) {
-      float v;
-      if constexpr (FP8)
-        v = whole || (row[kvh * kPgD + d] & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
-      else
-        v = bf_lo(reinterpret_cast<const uint16_t*>(row)[kvh * kPgD + d]);
-      if (isfinite(v)) continue;
-      if (out) out[d] = (uint16_t)(pack_bf16x2(bf_lo(out[d]) + v, 0.f) & 0xffffu);
-      else part[d] += v;
-    }
-  }
+// True in one lane of the warp, the same one every time.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
 }
 
 // A wait of a whole warp: every lane gets one answer.
@@ -298,19 +286,73 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code));
 }
 
+// A position's row of 128 bf16 values of one kv head of V.
+template <bool LINEAR>
+__device__ __forceinline__ const uint16_t* v_row(const uint8_t* __restrict__ vp, const int32_t* __restrict__ trow,
+                                                 int pos, int page_shift, int num_pages, int rb) {
+  if constexpr (LINEAR) {
+    return reinterpret_cast<const uint16_t*>(vp + (long long)pos * rb);
+  } else {
+    const int pg = checked_page(__ldg(trow + (pos >> page_shift)), num_pages, nullptr);
+    return reinterpret_cast<const uint16_t*>(
+        vp + (((long long)pg << page_shift) + (pos & ((1 << page_shift) - 1))) * rb);
+  }
+}
+
+// Rare: adds the infinities and NaN of the flagged V rows a token sees to its
+// finished row (bf16) or partial row (fp32), whichever is given.  vp: the
+// kv head's values in the pool, or in the sequence's window (LINEAR).
+template <bool LINEAR>
+__device__ __noinline__ void add_bad_rows(const uint8_t* __restrict__ vp, const int32_t* __restrict__ trow, int rb,
+                                          int page_shift, int num_pages, int first_masked, const uint32_t* bad,
+                                          int limit, uint16_t* out, float* part) {
+  for (int i = 0; i < kBadTiles * kTile; ++i) {
+    const int key = first_masked * kTile + i;
+    if (key > limit) break;
+    if (!((bad[i >> 5] >> (i & 31)) & 1u)) continue;
+    const uint16_t* row = v_row<LINEAR>(vp, trow, key, page_shift, num_pages, rb);
+    for (int d = 0; d < kPgD; ++d) {
+      const float v = bf_lo(row[d]);
+      if (isfinite(v)) continue;
+      if (out) out[d] = (uint16_t)(pack_bf16x2(bf_lo(out[d]) + v, 0.f) & 0xffffu);
+      else part[d] += v;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ softmax
 
-template <bool FP8>
+// Writes 64 bytes of each of a warp's 32 rows: lane r holds row r's (w), `at`
+// is its place in 64-byte units (-1: no such row).  Through shared memory, so
+// that four lanes write a row's 64 bytes side by side.
+__device__ __forceinline__ void store_rows(unsigned char* stage, const uint32_t* w, int at, unsigned char* dst) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    *reinterpret_cast<uint4*>(stage + lane * kStageRow + e * 16) =
+        make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r = e * 8 + (lane >> 2);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kStageRow + (lane & 3) * 16);
+    const int to = __shfl_sync(0xffffffffu, at, r);
+    if (to >= 0) *reinterpret_cast<uint4*>(dst + (long long)to * 64 + (lane & 3) * 16) = v;
+  }
+}
+
+template <bool LINEAR>
 __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, const TcPlan& pl, TcIter c, TcBars& bars,
                                              volatile int* abort_flag, int* err, float* part_o, float* part_ml,
-                                             float* scratch, uint32_t tmem) {
+                                             float* scratch, unsigned char* stage, uint32_t tmem) {
   const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t lanes = (uint32_t)(row & ~31) << 16;
   const uint32_t tS = tmem + x * kTile + lanes, tO = tmem + 2 * kTile + x * kTile + lanes;
   const float qs = a.qscale, lazy = fminf(8.f / qs, 1e30f);
   const int tr = row / a.G;   // this row's token in the tile
   const bool fits = row < pl.tpt * a.G;
-  uint32_t ns = 0, no = 0, items = 0;
+  uint32_t ns = 0, no = 0, items = 0;   // key tiles and pieces so far
   TcItem it;
   for (; next_item(a, pl, c, it); ++items) {
     const int cnt = x ? it.cntB : it.cntA;
@@ -320,16 +362,15 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
     const int limit = it.pos0 + t;
     const bool any = __any_sync(0xffffffffu, rowok);
     const int wmin = __reduce_min_sync(0xffffffffu, rowok ? limit : INT_MAX);
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;   // reference (of the scores), sum
     bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
-    for (int i = 0; i < cnt; ++i) {
+    for (int i = 0; i < cnt; ++i, ++ns) {
       const int kb = it.tile_of(x, i) * kTile;
       ok = warp_wait(&bars.s_full[x], ns & 1u, abort_flag, err, 34) && ok;
-      ++ns;
       if (ok && any) {
         tc_fence_after();
-        // one pass with the maximum so far; only when the tile's own exceeds
-        // it by more than 2^8 (and for the first tile) a second pass
+        // one pass with the reference so far; only when the tile's maximum
+        // exceeds it by more than 2^8 (and for the first tile) a second pass
         const int last = limit - kb;   // columns beyond it are masked
         const bool masked = kb + kTile - 1 > wmin;
         uint32_t p[64];
@@ -344,7 +385,7 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
           const float f = up ? ex2((m - mx) * qs) : 1.f;   // 0 when nothing was seen before
           if (up) m = mx;
           l *= f;
-          if (i > 0) {
+          if (i > 0) {   // (the products before are done: the scores came after them)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t o[32];
@@ -370,23 +411,22 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
       ++no;
       tc_fence_after();
     }
+    if (m != -INFINITY) m *= qs;   // base-2 logarithm from here on
     const bool direct = it.j0 == 0 && it.j1 == it.n;
     const bool join = it.split && it.cntB > 0;
-    float m2 = m == -INFINITY ? -INFINITY : m * qs;   // base-2 logarithm
     if (x && it.split) {
       if (join) {   // B's share goes to A through the CTA's scratch rows
         if (ok && any) {
-          float* dst = scratch + (size_t)row * (kPgD + 4);
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t o[32];
             tmem_ld32(tO + 32 * q, o);
             tmem_ld_wait32(o);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<uint4*>(dst + 32 * q)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 2; ++e)
+              store_rows(stage, o + 16 * e, row * 8 + 2 * q + e, reinterpret_cast<unsigned char*>(scratch));
           }
-          *reinterpret_cast<float2*>(dst + kPgD) = make_float2(m2, l);
+          *reinterpret_cast<float2*>(scratch + kTile * kPgD + row * 2) = make_float2(m, l);
         }
         tc_fence_before();
         named_sync(1, 256);
@@ -395,40 +435,41 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
       continue;
     }
     float fA = 1.f, fB = 0.f;
-    const float* other = scratch + (size_t)row * (kPgD + 4);
+    const float* other = scratch + (size_t)row * kPgD;
     if (join) {
       named_sync(1, 256);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(other + kPgD));
-      const float mb = ml.x, M = fmaxf(m2, mb);
-      fA = m2 == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m2 - M);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(scratch + kTile * kPgD + row * 2));
+      const float mb = ml.x, M = fmaxf(m, mb);
+      fA = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);
       fB = mb == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(mb - M);
       l = (fA != 0.f ? l * fA : 0.f) + (fB != 0.f ? ml.y * fB : 0.f);
-      m2 = M;
+      m = M;
     }
-    const int tok = it.tok0 + t, head = it.kvh * a.G + row % a.G;
-    uint16_t* orow = a.out + ((long long)tok * a.Hq + head) * kPgD;
+    const int tok = it.tok0 + t, head = (pl.h0 + it.kvh) * a.G + row % a.G;
+    const long long orow = (long long)tok * a.Hq + head;
     // the piece's slot: 0 continues an item of the CTAs before, 1 is continued by the next
     const long long slot = 2ll * blockIdx.x + (it.j0 > 0 ? 0 : 1);
-    float* prow = part_o + (slot * 2 * kTile + x * kTile + row) * kPgD;
+    float* part = part_o + slot * 2 * kTile * kPgD;
+    const int prow = x * kTile + row;
     if (direct) {
       const bool none = l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
       fA *= inv;
       fB *= inv;
     }
-    const bool dead = fA == 0.f;   // nothing seen: what O holds does not count
+    const bool dead = fA == 0.f || cnt == 0;   // nothing seen: what O holds does not count
     if (any) {
+      // (the item's first row of this warp is the base: rows of a warp lie
+      // within 32-bit distances of 64-byte units)
+      const long long base = __shfl_sync(0xffffffffu, orow, 0);
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * q, o);
         tmem_ld_wait32(o);
-        if (rowok) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float v = __uint_as_float(o[e]);
-          o[e] = __float_as_uint(!ok ? __uint_as_float(0x7fc00000u) : dead || cnt == 0 ? 0.f : v * fA);
-        }
+        for (int e = 0; e < 32; ++e)
+          o[e] = __float_as_uint(!ok ? __uint_as_float(0x7fc00000u) : dead ? 0.f : __uint_as_float(o[e]) * fA);
         if (join && fB != 0.f) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -440,30 +481,23 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
           }
         }
         if (direct) {
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              w[u] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * u]), __uint_as_float(o[8 * e + 2 * u + 1]));
-            reinterpret_cast<uint4*>(orow + 32 * q)[e] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          store_rows(stage, w, rowok ? (int)(orow - base) * 4 + q : -1,
+                     reinterpret_cast<unsigned char*>(a.out + base * kPgD));
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<uint4*>(prow + 32 * q)[e] =
-                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 2; ++e)
+            store_rows(stage, o + 16 * e, rowok ? prow * 8 + 2 * q + e : -1, reinterpret_cast<unsigned char*>(part));
         }
-        }
-        __syncwarp();
       }
     }
     if (rowok) {
       if (!direct)
-        *reinterpret_cast<float2*>(part_ml + (slot * 2 * kTile + x * kTile + row) * 2) = make_float2(m2, l);
+        *reinterpret_cast<float2*>(part_ml + (slot * 2 * kTile + prow) * 2) = make_float2(m, l);
       else if (a.lse != nullptr)
-        a.lse[(long long)tok * a.Hq + head] =
-            !ok ? __uint_as_float(0x7fc00000u) : (l == 0.f ? -INFINITY : (m2 + log2f(l)) * kPgLn2);
+        a.lse[orow] = !ok ? __uint_as_float(0x7fc00000u) : (l == 0.f ? -INFINITY : (m + log2f(l)) * kPgLn2);
       const uint32_t(*bad)[4] = bars.bad[items % kBadRing];
       uint32_t flagged = 0u;
 #pragma unroll
@@ -471,9 +505,15 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
         const uint4 w = *reinterpret_cast<const uint4*>(bad[e]);
         flagged |= w.x | w.y | w.z | w.w;
       }
-      if (flagged && ok)
-        add_bad_rows<FP8>(a.vp, a.table + (long long)it.b * a.max_pages, a.Hkv, it.kvh, a.page_shift, a.num_pages,
-                          it.first_masked(), bad[0], limit, direct ? orow : nullptr, prow);
+      if (flagged && ok) {
+        const uint8_t* vp = LINEAR ? reinterpret_cast<const uint8_t*>(
+                                         pl.vw + ((long long)(it.b - pl.b0) * pl.cap * pl.nh + it.kvh) * kPgD)
+                                   : a.vp + (pl.h0 + it.kvh) * (2 * kPgD);
+        add_bad_rows<LINEAR>(vp, a.table + (long long)it.b * a.max_pages,
+                             LINEAR ? pl.nh * (2 * kPgD) : paged_row_bytes(0, a.Hkv), a.page_shift, a.num_pages,
+                             it.first_masked(), bad[0], limit, direct ? a.out + orow * kPgD : nullptr,
+                             part + (long long)prow * kPgD);
+      }
     }
     tc_fence_before();   // O is read before the next item's first product overwrites it
     if (join) named_sync(2, 256);
@@ -492,52 +532,32 @@ constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
 
-// True in one lane of the warp, the same one every time.
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok));
-  return ok != 0;
-}
-
 // One elected lane walks the items, waits and issues.  Waits cost a few hundred
 // clocks each on this path, during which the tensor core runs dry, so each
 // tile is waited for once (by the first of A and B that uses it) and before
 // the wait for P, and a product pair O += P V, S = Q K'^T is issued in one go.
 __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, TcIter c, TcBars& bars,
-                                         volatile int* abort_flag, int* err, unsigned char* sQ, unsigned char* sK,
-                                         unsigned char* sV, const uint32_t tmem, const bool fp8) {
+                                         volatile int* abort_flag, int* err, uint32_t sQ, uint32_t sK, uint32_t sV,
+                                         const uint32_t tmem) {
   constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kTile);
   constexpr uint32_t kIdO = kIdS | (1u << 16);   // V: the reduction index is the row
-  const uint32_t q_lo = kDescLoK | (smem_u32(sQ) >> 4), k_lo = kDescLoK | (smem_u32(sK) >> 4),
-                 v_lo = kDescLoV | (smem_u32(sV) >> 4);
-  uint32_t seq0 = 0, nq[2] = {0, 0}, np[2] = {0, 0}, clean = 0u;
+  const uint32_t q_lo = kDescLoK | (sQ >> 4), k_lo = kDescLoK | (sK >> 4), v_lo = kDescLoV | (sV >> 4);
+  uint32_t seq0 = 0, nq[2] = {0, 0}, np[2] = {0, 0};
   uint32_t k_seen = 0, v_seen = 0;   // key tiles known to be in shared memory
-  TcItem it;
+  TcItem it = {};
   bool ok = true;
-  auto seq_of = [&](int x, int i) { return seq0 + (uint32_t)(it.tile_of(x, i) - it.j0); };
   auto need_k = [&](uint32_t seq) {
-    if (seq < k_seen) return;
-    ok = ok && mbar_wait(&bars.k_full[seq % kStages], (seq / kStages) & 1u, abort_flag, err, 36);
-    k_seen = seq + 1;
+    for (; k_seen <= seq; ++k_seen)
+      ok = ok && mbar_wait(&bars.k_full[k_seen % kStages], (k_seen / kStages) & 1u, abort_flag, err, 36);
   };
-  auto need_v = [&](uint32_t seq, bool masked) {
-    if (seq < v_seen) return;
-    const uint32_t s = seq % kStages;
-    ok = ok && mbar_wait(&bars.v_full[s], (seq / kStages) & 1u, abort_flag, err, 38);
-    if (!fp8 && masked) {   // cleaned first
-      ok = ok && mbar_wait(&bars.v_clean[s], (clean >> s) & 1u, abort_flag, err, 39);
-      clean ^= 1u << s;
-    }
-    v_seen = seq + 1;
+  auto need_v = [&](uint32_t seq) {
+    for (; v_seen <= seq; ++v_seen)
+      ok = ok && mbar_wait(&bars.v_clean[v_seen % kStages], (v_seen / kStages) & 1u, abort_flag, err, 38);
   };
   // scores of tile x against the key tile `seq`
   auto qk = [&](int x, uint32_t seq) {
     const uint32_t s = seq % kStages;
-    const uint32_t ql = q_lo + (x && !it.split ? kTileBytes >> 4 : 0u), kl = k_lo + s * (kTileBytes >> 4);
+    const uint32_t ql = q_lo + x * (kTileBytes >> 4), kl = k_lo + s * (kTileBytes >> 4);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       const uint32_t off = (((uint32_t)ks >> 2) * kHalfBytes + ((uint32_t)ks & 3u) * 32u) >> 4;
@@ -549,27 +569,27 @@ __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, T
   while (ok && next_item(a, pl, c, it)) {
     const int cnt[2] = {it.cntA, it.cntB};
     const int most = max(cnt[0], cnt[1]);
-    const int first_masked = it.first_masked();
+    const uint32_t mul = it.split ? 2u : 1u;   // tile i of A is mul * i, of B one on when split
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       if (cnt[x] == 0) continue;
-      if (x == 0 || !it.split) {
-        ok = ok && mbar_wait(&bars.q_full[x], nq[x] & 1u, abort_flag, err, 37);
-        ++nq[x];
-      }
-      need_k(seq_of(x, 0));
+      const uint32_t seq = seq0 + (it.split ? x : 0);
+      ok = ok && mbar_wait(&bars.q_full[x], nq[x] & 1u, abort_flag, err, 37);
+      ++nq[x];
+      need_k(seq);
       if (!ok) break;
       tc_fence_after();
-      qk(x, seq_of(x, 0));
+      qk(x, seq);
+      if (cnt[x] == 1) umma_commit(&bars.q_empty[x]);
     }
     for (int i = 0; i < most && ok; ++i) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (i >= cnt[x]) continue;
-        const uint32_t seq = seq_of(x, i), s = seq % kStages;
+        const uint32_t seq = seq0 + mul * i + (it.split ? x : 0), s = seq % kStages;
         const bool end = i + 1 == cnt[x];
-        need_v(seq, it.tile_of(x, i) >= first_masked);
-        if (!end) need_k(seq_of(x, i + 1));
+        need_v(seq);
+        if (!end) need_k(seq + mul);
         ok = ok && mbar_wait(&bars.p_full[x], np[x] & 1u, abort_flag, err, 40);
         if (!ok) break;
         ++np[x];
@@ -580,10 +600,9 @@ __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, T
           umma_bf16_ts(tmem + 2 * kTile + x * kTile, tmem + x * kTile + ks * 8, desc_of(vl + ks * (2048u >> 4)), kIdO,
                        i > 0 || ks > 0);
         if (x || it.split) umma_commit(&bars.v_empty[s]);
-        if (!end) qk(x, seq_of(x, i + 1));
+        if (!end) qk(x, seq + mul);
         else umma_commit(&bars.o_full[x]);
-        // Q is free once its last scores are done
-        if (it.split ? x == 0 && end : i + 2 == cnt[x] || cnt[x] == 1) umma_commit(&bars.q_empty[x]);
+        if (i + 2 == cnt[x]) umma_commit(&bars.q_empty[x]);   // the queries' last product
       }
     }
     seq0 += (uint32_t)(it.j1 - it.j0);
@@ -597,7 +616,7 @@ __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, T
 
 // ------------------------------------------------------------------- kernel
 
-template <bool FP8>
+template <bool LINEAR>
 __global__ void __launch_bounds__(kTcThreads, 1)
 paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const PagedArgs a, const TcPlan pl,
@@ -608,8 +627,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   unsigned char* sQ = base;                                   // tiles A, B
   unsigned char* sK = sQ + 2 * kTileBytes;
   unsigned char* sV = sK + kStages * kTileBytes;
-  unsigned char* sRaw = sV + kStages * kTileBytes;            // E4M3: K codes, V codes
-  TcBars& bars = *reinterpret_cast<TcBars*>(sRaw + (FP8 ? 2 * kRawBytes : 0));
+  TcBars& bars = *reinterpret_cast<TcBars*>(sV + kStages * kTileBytes);
+  unsigned char* stage = sV + kStages * kTileBytes + 1024;    // output rows, a part per softmax warp
   volatile int* abort_flag = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -622,16 +641,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       mbar_init(&bars.o_full[i], 1);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bars.k_full[i], FP8 ? 4 : 1);
+      mbar_init(&bars.k_full[i], 1);
       mbar_init(&bars.k_empty[i], 1);
-      mbar_init(&bars.v_full[i], FP8 ? 4 : 1);
+      mbar_init(&bars.v_full[i], 1);
       mbar_init(&bars.v_empty[i], 1);
       mbar_init(&bars.v_clean[i], 4);
     }
-    mbar_init(&bars.rk_full, 1);
-    mbar_init(&bars.rk_empty, 4);
-    mbar_init(&bars.rv_full, 1);
-    mbar_init(&bars.rv_empty, 4);
     mbar_init(&bars.drain, 1);
     bars.abort = 0;
     fence_barrier_init();
@@ -649,7 +664,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   const int per = (pl.P + kTcThreads - 1) / kTcThreads;
   const int p0 = min((int)threadIdx.x * per, pl.P), p1 = min(p0 + per, pl.P);
   int mine = 0;
-  for (int p = p0; p < p1; ++p) mine += item_span(a, pl, p / pl.nqb, p % pl.nqb, sp, nt);
+  for (int p = p0; p < p1; ++p) mine += item_span(a, pl, pl.b0 + p / pl.nqb, p % pl.nqb, sp, nt);
   long long before = 0, S = 0;
   {
     long long v = mine;
@@ -669,14 +684,14 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     }
     before += v - mine;
   }
-  const long long U = S * a.Hkv, Weff = U < pl.W ? U : pl.W;
+  const long long U = S * pl.nh, Weff = U < pl.W ? U : pl.W;
   const bool idle = (long long)blockIdx.x >= Weff;
   const long long lo = idle ? 0 : blockIdx.x * U / Weff, hi = idle ? 0 : (blockIdx.x + 1) * U / Weff;
   const long long r = idle ? 0 : lo % S;
   if (!idle && before <= r && r < before + mine) {
     long long at = before;
     for (int p = p0; p < p1; ++p) {
-      const int n = item_span(a, pl, p / pl.nqb, p % pl.nqb, sp, nt);
+      const int n = item_span(a, pl, pl.b0 + p / pl.nqb, p % pl.nqb, sp, nt);
       if (r < at + n) {
         bars.plan[0] = p / pl.nqb;
         bars.plan[1] = p % pl.nqb;
@@ -702,61 +717,68 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     if (next_item(a, pl, c2, it)) pc = {it.b, it.qb, it.kvh, it.j0, it.j1, it.n, 1, 0};
     pieces[blockIdx.x] = pc;
   }
-  float* my_scratch = scratch + (size_t)blockIdx.x * kTile * (kPgD + 4);
-  const int rb = paged_row_bytes(FP8, a.Hkv);
+  float* my_scratch = scratch + (size_t)blockIdx.x * kTile * (kPgD + 2);
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role<FP8>(warp >> 2, a, pl, c, bars, abort_flag, err, part_o, part_ml, my_scratch, tmem);
+    softmax_role<LINEAR>(warp >> 2, a, pl, c, bars, abort_flag, err, part_o, part_ml, my_scratch,
+                         stage + warp * 32 * kStageRow, tmem);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
       // ---------------------------------------------------- K and V loads
       uint32_t seq = 0, issued[2] = {0, 0};
-      const int page_rows = 1 << a.page_shift, piece = min(kTile, page_rows);
+      const int page_rows = LINEAR ? kTile : 1 << a.page_shift, piece = min(kTile, page_rows);
       const int pieces_per_tile = kTile / piece;
-      const uint32_t piece_bytes = (uint32_t)piece * 128u;   // of one half (bf16) or of all codes
+      const uint32_t piece_bytes = (uint32_t)piece * 128u;   // of one half
       TcItem it;
       bool ok = true;
       while (ok && next_item(a, pl, c, it)) {
         const int32_t* trow = a.table + (long long)it.b * a.max_pages;
-        const int e_last = it.top > 0 ? (it.top - 1) >> a.page_shift : 0;
+        const int e_last = !LINEAR && it.top > 0 ? (it.top - 1) >> a.page_shift : 0;
         int e0 = it.j0 * kTile >> a.page_shift;
-        int pg = e0 + lane <= e_last ? __ldg(trow + e0 + lane) : 0;
-        int pg_next = e0 + 32 + lane <= e_last ? __ldg(trow + e0 + 32 + lane) : 0;
+        int pg = 0, pg_next = 0;
+        if constexpr (!LINEAR) {
+          pg = e0 + lane <= e_last ? __ldg(trow + e0 + lane) : 0;
+          pg_next = e0 + 32 + lane <= e_last ? __ldg(trow + e0 + 32 + lane) : 0;
+        }
         for (int j = it.j0; j < it.j1 && ok; ++j, ++seq) {
-          const int first = j * kTile >> a.page_shift;
-          if (first >= e0 + 32) {
-            e0 += 32;
-            pg = pg_next;
-            pg_next = e0 + 32 + lane <= e_last ? __ldg(trow + e0 + 32 + lane) : 0;
-          }
           // lane: piece (lane / 2) % 16 of the tile, half lane % 2
           const int pi = lane >> 1, half = lane & 1;
-          const int page = __shfl_sync(0xffffffffu, pg, (first - e0 + pi) & 31);
-          // pieces past the last key any token sees are not read
-          const int live = min(pieces_per_tile, max(0, (it.top - j * kTile + piece - 1) / piece));
-          const bool on = pi < live && (!FP8 || half == 0);
-          const int y = on ? (checked_page(page, a.num_pages, a.dbg) << a.page_shift) +
-                                 (j * kTile + pi * piece & (page_rows - 1))
-                           : 0;
+          int y, live, xc;
+          if constexpr (LINEAR) {
+            live = 1;
+            y = (int)((it.b - pl.b0) * pl.cap) + j * kTile;
+            xc = it.kvh * kPgD + half * 64;
+          } else {
+            const int first = j * kTile >> a.page_shift;
+            if (first >= e0 + 32) {
+              e0 += 32;
+              pg = pg_next;
+              pg_next = e0 + 32 + lane <= e_last ? __ldg(trow + e0 + 32 + lane) : 0;
+            }
+            const int page = __shfl_sync(0xffffffffu, pg, (first - e0 + pi) & 31);
+            // pieces past the last key any token sees are not read
+            live = min(pieces_per_tile, max(0, (it.top - j * kTile + piece - 1) / piece));
+            y = pi < live ? (checked_page(page, a.num_pages, a.dbg) << a.page_shift) +
+                                (j * kTile + pi * piece & (page_rows - 1))
+                          : 0;
+            xc = (pl.h0 + it.kvh) * kPgD + half * 64;
+          }
+          const bool on = pi < live;
+          const uint32_t s = seq % kStages;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            uint64_t* full = FP8 ? (kv ? &bars.rv_full : &bars.rk_full)
-                                 : (kv ? &bars.v_full[seq % kStages] : &bars.k_full[seq % kStages]);
-            uint64_t* empty = FP8 ? (kv ? &bars.rv_empty : &bars.rk_empty)
-                                  : (kv ? &bars.v_empty[seq % kStages] : &bars.k_empty[seq % kStages]);
-            const uint32_t use = FP8 ? seq : seq / kStages;
-            if (use > 0 && !warp_wait(empty, (use - 1) & 1u, abort_flag, err, 31)) {
+            uint64_t* full = kv ? &bars.v_full[s] : &bars.k_full[s];
+            if (seq >= kStages && !warp_wait(kv ? &bars.v_empty[s] : &bars.k_empty[s], (seq / kStages - 1) & 1u,
+                                             abort_flag, err, 31)) {
               ok = false;
               break;
             }
-            unsigned char* dst = FP8 ? sRaw + kv * kRawBytes + pi * piece_bytes
-                                     : (kv ? sV : sK) + (seq % kStages) * kTileBytes + half * kHalfBytes +
-                                           pi * piece_bytes;
-            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * piece_bytes * (FP8 ? 1u : 2u));
+            unsigned char* dst = (kv ? sV : sK) + s * kTileBytes + half * kHalfBytes + pi * piece_bytes;
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * piece_bytes * 2u);
             __syncwarp();
-            if (on) tma_load_2d(dst, kv ? &map_v : &map_k, full, it.kvh * kPgD + (FP8 ? 0 : half * 64), y);
+            if (on) tma_load_2d(dst, kv ? &map_v : &map_k, full, xc, y);
             issued[kv] = seq + 1;
           }
         }
@@ -764,16 +786,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       if (!ok || *abort_flag) {   // after an abort: copies in flight land before the CTA exits
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv)
-          for (uint32_t i = issued[kv] > kStages ? issued[kv] - kStages : 0; i < issued[kv]; ++i) {
-            // E4M3 has one raw tile per cache, bf16 a tile per stage
-            if (FP8 && i + 1 < issued[kv]) continue;
-            uint64_t* full = FP8 ? (kv ? &bars.rv_full : &bars.rk_full)
-                                 : (kv ? &bars.v_full[i % kStages] : &bars.k_full[i % kStages]);
-            if (!mbar_wait_drain(full, (FP8 ? i : i / kStages) & 1u) && err) atomicCAS(err, 0, 44);
-          }
+          for (uint32_t i = issued[kv] > kStages ? issued[kv] - kStages : 0; i < issued[kv]; ++i)
+            if (!mbar_wait_drain(kv ? &bars.v_full[i % kStages] : &bars.k_full[i % kStages], (i / kStages) & 1u) && err)
+              atomicCAS(err, 0, 44);
       }
     } else if (warp == 9) {
-      if (elect_lane()) mma_role(a, pl, c, bars, abort_flag, err, sQ, sK, sV, tmem, FP8);
+      if (elect_lane()) mma_role(a, pl, c, bars, abort_flag, err, smem_u32(sQ), smem_u32(sK), smem_u32(sV), tmem);
       __syncwarp();
     } else if (warp == 10) {
       // ------------------------------------------------------------ Q loads
@@ -785,7 +803,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         while (ok && next_item(a, pl, c, it)) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (!ok || (x == 0 ? it.cntA == 0 : it.split)) continue;
+            if (!ok || (x ? it.cntB : it.cntA) == 0) continue;   // (a split item's rows go to both)
             if (nq[x] > 0 && !mbar_wait(&bars.q_empty[x], (nq[x] - 1) & 1u, abort_flag, err, 32)) {
               ok = false;
               continue;
@@ -794,8 +812,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             mbar_arrive_expect_tx(&bars.q_full[x], bytes);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              tma_load_3d(sQ + x * kTileBytes + h * kHalfBytes, &map_q, &bars.q_full[x], h * 64, it.kvh * a.G,
-                          it.tok0 + x * pl.tpt);
+              tma_load_3d(sQ + x * kTileBytes + h * kHalfBytes, &map_q, &bars.q_full[x], h * 64,
+                          (pl.h0 + it.kvh) * a.G, it.tok0 + (it.split ? 0 : x * pl.tpt));
           }
         }
         if (!ok || *abort_flag)
@@ -806,7 +824,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    // ------------------------------ V cleaning; E4M3: codes to bf16 operands
+    // ------------------------------------------------------- V cleaning
+    // Every tile is handed on from here, cleaned or not: these warps never
+    // fall behind a barrier's phases.
     const int t = threadIdx.x & 127;   // row of the tile
     const uint32_t sw = (uint32_t)(t & 7);
     uint32_t seq = 0, items = 0;
@@ -818,103 +838,39 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       named_sync(3, 128);
       const int first_masked = it.first_masked();
       for (int j = it.j0; j < it.j1 && ok; ++j, ++seq) {
-        const uint32_t s = seq % kStages, ph = (seq / kStages) & 1u;
+        const uint32_t s = seq % kStages;
+        ok = warp_wait(&bars.v_full[s], (seq / kStages) & 1u, abort_flag, err, 33);
+        if (!ok) break;
         const int key = j * kTile + t;
-        const bool masked = j >= first_masked;
         unsigned char* vrow = sV + s * kTileBytes + (uint32_t)t * 128u;
         bool flag = false;
-        if constexpr (!FP8) {
-          ok = warp_wait(&bars.v_full[s], ph, abort_flag, err, 33);
-          if (!ok) break;
-          if (masked) {
-            if (key >= it.top) {
+        if (j < first_masked) {   // seen by all: handed on as it is
+        } else if (key >= it.top) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                *reinterpret_cast<uint4*>(vrow + (e >> 3) * kHalfBytes + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            } else if (key > it.pos0) {
+          for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<uint4*>(vrow + (e >> 3) * kHalfBytes + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        } else if (key > it.pos0) {
 #pragma unroll 4
-              for (int e = 0; e < 16; ++e) {
-                uint4* p = reinterpret_cast<uint4*>(vrow + (e >> 3) * kHalfBytes + (((uint32_t)e & 7u) ^ sw) * 16);
-                uint4 v = *p;
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                bool hit = false;
+          for (int e = 0; e < 16; ++e) {
+            uint4* p = reinterpret_cast<uint4*>(vrow + (e >> 3) * kHalfBytes + (((uint32_t)e & 7u) ^ sw) * 16);
+            const uint4 v = *p;
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            bool hit = false;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  if ((w[u] & 0x7f80u) == 0x7f80u) w[u] &= 0xffff0000u, hit = true;
-                  if ((w[u] & 0x7f800000u) == 0x7f800000u) w[u] &= 0x0000ffffu, hit = true;
-                }
-                if (hit) {
-                  *p = make_uint4(w[0], w[1], w[2], w[3]);
-                  flag = true;
-                }
-              }
+            for (int u = 0; u < 4; ++u) {
+              if ((w[u] & 0x7f80u) == 0x7f80u) w[u] &= 0xffff0000u, hit = true;
+              if ((w[u] & 0x7f800000u) == 0x7f800000u) w[u] &= 0x0000ffffu, hit = true;
             }
-            if (flag) atomicOr(&bad[j - first_masked][t >> 5], 1u << (t & 31));
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.v_clean[s]);
-          }
-        } else {
-          const bool seen = key < it.top;
-          uint32_t sck = 0u, scv = 0u;
-          if (seen) {
-            const long long off =
-                row_offset(a.table + (long long)it.b * a.max_pages, key, a.page_shift, a.num_pages, rb, a.dbg);
-            sck = __ldg(a.kp + off + a.Hkv * kPgD + it.kvh);
-            scv = __ldg(a.vp + off + a.Hkv * kPgD + it.kvh);
-          }
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = ok && warp_wait(kv ? &bars.rv_full : &bars.rk_full, seq & 1u, abort_flag, err, 42);
-            if (!ok) break;
-            const unsigned char* raw = sRaw + kv * kRawBytes + (uint32_t)t * 128u;
-            uint4 cd[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              cd[e] = *reinterpret_cast<const uint4*>(raw + (((uint32_t)e ^ sw) * 16));
-            if (seq >= kStages)
-              ok = warp_wait(kv ? &bars.v_empty[s] : &bars.k_empty[s], ph ^ 1u, abort_flag, err, 43);
-            if (!ok) break;
-            const float sc = e8m0_value(kv ? scv : sck);
-            const bool partial = kv && masked && key > it.pos0;   // some token does not see this row
-            unsigned char* drow = (kv ? sV : sK) + s * kTileBytes + (uint32_t)t * 128u;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {   // 16 codes -> two 16-byte chunks of bf16
-              const uint32_t w[4] = {cd[e].x, cd[e].y, cd[e].z, cd[e].w};
-              uint32_t o[8];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                o[2 * u] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[u] & 0xffffu), sc);
-                o[2 * u + 1] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[u] >> 16), sc);
-              }
-              if (kv && partial) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                  if ((o[u] & 0x7f80u) == 0x7f80u) o[u] &= 0xffff0000u, flag = true;
-                  if ((o[u] & 0x7f800000u) == 0x7f800000u) o[u] &= 0x0000ffffu, flag = true;
-                }
-              }
-              if (kv && !seen) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) o[u] = 0u;
-              }
-              unsigned char* d = drow + (e >> 2) * kHalfBytes;
-              const uint32_t c0 = (uint32_t)(2 * e) & 7u;
-              *reinterpret_cast<uint4*>(d + ((c0 ^ sw) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(d + (((c0 + 1) ^ sw) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            if (kv && flag && seen) atomicOr(&bad[j - first_masked][t >> 5], 1u << (t & 31));
-            fence_proxy_async();
-            __syncwarp();
-            // the raw tile is given back only here, when what was read of it has
-            // been used: given back right behind the loads, rows of the next
-            // tile were seen in it
-            if (lane == 0) {
-              mbar_arrive(kv ? &bars.v_full[s] : &bars.k_full[s]);
-              mbar_arrive(kv ? &bars.rv_empty : &bars.rk_empty);
+            if (hit) {
+              *p = make_uint4(w[0], w[1], w[2], w[3]);
+              flag = true;
             }
           }
         }
+        if (flag) atomicOr(&bad[j - first_masked][t >> 5], 1u << (t & 31));
+        if (j >= first_masked) fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.v_clean[s]);
       }
     }
   }
@@ -924,8 +880,50 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
+// The rows of E4M3 sequences [b0, b0 + nb) and kv heads [h0, h0 + nh) in
+// bf16: one warp per position (K and V).
+__global__ void __launch_bounds__(256)
+paged_window_kernel(const PagedArgs a, const TcPlan pl, uint16_t* __restrict__ kw, uint16_t* __restrict__ vw) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = blockIdx.x * 8 + (threadIdx.x >> 5), warps = gridDim.x * 8;
+  const int rb = paged_row_bytes(1, a.Hkv), page_mask = (1 << a.page_shift) - 1;
+  for (int b = pl.b0; b < pl.b0 + pl.nb; ++b) {
+    const SeqSpan s = seq_span(a.q_start, a.kv_len, b, a.N, a.max_pages << a.page_shift);
+    if (s.len == 0) continue;
+    for (int pos = warp; pos < s.kv; pos += warps) {
+      const int pg = checked_page(__ldg(a.table + (long long)b * a.max_pages + (pos >> a.page_shift)), a.num_pages,
+                                  a.dbg);
+      const long long off = (((long long)pg << a.page_shift) + (pos & page_mask)) * rb;
+      const long long to = ((long long)(b - pl.b0) * pl.cap + pos) * pl.nh * kPgD;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint8_t* row = (kv ? a.vp : a.kp) + off;
+        uint16_t* dst = (kv ? vw : kw) + to;
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {   // 8 lanes per head, 16 codes per lane
+          const int h = 4 * it + (lane >> 3), j = lane & 7;
+          if (h >= pl.nh) break;
+          const uint4 c = __ldg(reinterpret_cast<const uint4*>(row + (pl.h0 + h) * kPgD) + j);
+          const float sc = e8m0_value(row[a.Hkv * kPgD + pl.h0 + h]);
+          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+          uint32_t r[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            r[2 * i] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[i] & 0xffffu), sc);
+            r[2 * i + 1] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[i] >> 16), sc);
+          }
+          uint4* d = reinterpret_cast<uint4*>(dst + h * kPgD + j * 16);
+          d[0] = make_uint4(r[0], r[1], r[2], r[3]);
+          d[1] = make_uint4(r[4], r[5], r[6], r[7]);
+        }
+      }
+    }
+  }
+}
+
 // Joins the pieces of items that several CTAs share.  Block (c, g): the item
-// that CTA c is the first to continue; rows g * 32 .. + 31, a warp per row.
+// that CTA c is the first to continue; rows g * 32 .. + 31, four per warp.
 __global__ void __launch_bounds__(256)
 paged_tc_merge_kernel(const PagedArgs a, const TcPlan pl, const TcPiece* __restrict__ pieces,
                       const float* __restrict__ part_o, const float* __restrict__ part_ml,
@@ -937,61 +935,94 @@ paged_tc_merge_kernel(const PagedArgs a, const TcPlan pl, const TcPiece* __restr
   if (!me.valid || me.j0 == 0) return;
   auto same = [&](const TcPiece& o) { return o.valid && o.b == me.b && o.qb == me.qb && o.kvh == me.kvh; };
   if (same(prev) && prev.j0 > 0) return;   // not the first to continue it
-  int last = c;                            // the piece that ends the item
-  for (int end = me.j1; end < me.n;) {
-    ++last;
-    if (last >= pl.W) return;              // (never: the pieces cover the item)
-    end = pieces[last].j1;
-  }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int C = last - c + 2;
-  // contributor i: the beginning (slot 1 of CTA c - 1), then slot 0 of CTAs c ..
-  auto slot = [&](int i) { return i == 0 ? 2ll * (c - 1) + 1 : 2ll * (c - 1 + i); };
-  const bool failed = *err != 0;
   SeqSpan s;
   int nt;
   item_span(a, pl, me.b, me.qb, s, nt);
-  for (int q = 0; q < 4; ++q) {
-    const int row = blockIdx.y * 32 + q * 8 + warp;
-    const int x = row >> 7, rr = row & 127, tr = rr / a.G;
-    const int t = x * pl.tpt + tr;
-    if (rr >= pl.tpt * a.G || t >= nt) continue;
-    float M = -INFINITY;
-    for (int i = lane; i < C; i += 32) M = fmaxf(M, __ldcg(part_ml + (slot(i) * 2 * kTile + row) * 2));
-    M = warp_max(M);
-    float L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < C; ++i) {
-      const long long at = slot(i) * 2 * kTile + row;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml + at * 2));
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(part_o + at * kPgD) + lane);
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;
-      const float w = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);   // (a NaN sum counts)
-      if (w == 0.f) continue;
-      L = fmaf(ml.y, w, L);
-      o.x = fmaf(v.x, w, o.x);
-      o.y = fmaf(v.y, w, o.y);
-      o.z = fmaf(v.z, w, o.z);
-      o.w = fmaf(v.w, w, o.w);
+  constexpr int kRows = 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row0 = blockIdx.y * 32 + warp * kRows;
+  long long at[kRows];
+  bool on[kRows], any = false;
+#pragma unroll
+  for (int q = 0; q < kRows; ++q) {
+    const int x = (row0 + q) >> 7, rr = (row0 + q) & 127, t = x * pl.tpt + rr / a.G;
+    on[q] = rr < pl.tpt * a.G && t < nt;
+    any |= on[q];
+    at[q] = (long long)(s.begin + me.qb * pl.tpi + t) * a.Hq + (pl.h0 + me.kvh) * a.G + rr % a.G;
+  }
+  if (!any) return;
+  float M[kRows], L[kRows];
+  float4 o[kRows];
+#pragma unroll
+  for (int q = 0; q < kRows; ++q) {
+    M[q] = -INFINITY;
+    L[q] = 0.f;
+    o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // the beginning (slot 1 of CTA c - 1), then slot 0 of CTAs c .. to the one that ends the item
+  int end = 0;
+  for (int i = 0; end < me.n; ++i) {
+    const long long slot = i == 0 ? 2ll * (c - 1) + 1 : 2ll * (c - 1 + i);
+    float2 ml[kRows];
+    float4 v[kRows];
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      const long long r = slot * 2 * kTile + row0 + q;
+      ml[q] = on[q] ? __ldcg(reinterpret_cast<const float2*>(part_ml + r * 2)) : make_float2(-INFINITY, 0.f);
+      v[q] = on[q] ? __ldcg(reinterpret_cast<const float4*>(part_o + r * kPgD) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const bool none = L == 0.f;
-    const float inv = failed ? __uint_as_float(0x7fc00000u) : (none ? 0.f : 1.f / L);
-    const long long at = (long long)(s.begin + me.qb * pl.tpi + t) * a.Hq + me.kvh * a.G + rr % a.G;
-    reinterpret_cast<uint2*>(a.out + at * kPgD)[lane] =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    end = i == 0 ? me.j0 : pieces[c - 1 + i].j1;
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      if (ml[q].x == -INFINITY && ml[q].y == 0.f) continue;   // this piece saw nothing (a NaN sum counts)
+      const float m = fmaxf(M[q], ml[q].x);
+      const float f = M[q] == -INFINITY ? (L[q] == 0.f ? 0.f : 1.f) : exp2f(M[q] - m);
+      const float w = ml[q].x == -INFINITY ? 1.f : exp2f(ml[q].x - m);
+      M[q] = m;
+      L[q] = (f != 0.f ? L[q] * f : 0.f) + (w != 0.f ? ml[q].y * w : 0.f);
+      auto fold = [&](float acc, float x) { return (f != 0.f ? acc * f : 0.f) + (w != 0.f ? x * w : 0.f); };
+      o[q].x = fold(o[q].x, v[q].x);
+      o[q].y = fold(o[q].y, v[q].y);
+      o[q].z = fold(o[q].z, v[q].z);
+      o[q].w = fold(o[q].w, v[q].w);
+    }
+  }
+  const bool failed = *err != 0;
+#pragma unroll
+  for (int q = 0; q < kRows; ++q) {
+    if (!on[q]) continue;
+    const bool none = L[q] == 0.f;
+    const float inv = failed ? __uint_as_float(0x7fc00000u) : (none ? 0.f : 1.f / L[q]);
+    reinterpret_cast<uint2*>(a.out + at[q] * kPgD)[lane] =
+        make_uint2(pack_bf16x2(o[q].x * inv, o[q].y * inv), pack_bf16x2(o[q].z * inv, o[q].w * inv));
     if (lane == 0 && a.lse != nullptr)
-      a.lse[at] = failed ? __uint_as_float(0x7fc00000u) : (none ? -INFINITY : (M + log2f(L)) * kPgLn2);
+      a.lse[at[q]] = failed ? __uint_as_float(0x7fc00000u) : (none ? -INFINITY : (M[q] + log2f(L[q])) * kPgLn2);
   }
 }
 
-TcPlan tc_plan(int B, int G, int max_q) {
-  TcPlan pl;
+// Windows of an E4M3 call hold at most this much (or one kv head of one
+// sequence).
+constexpr long long kWindowBytes = 1ll << 30;
+
+TcPlan tc_plan(int fp8, int B, int Hkv, int G, int max_q, long long capacity) {
+  TcPlan pl = {};
   pl.tpt = kTile / G;
   pl.tpi = 2 * pl.tpt;
   pl.nqb = (max_q + pl.tpi - 1) / pl.tpi;
-  pl.P = B * pl.nqb;
   pl.W = device_sm_count();
+  pl.cap = (capacity + kTile - 1) / kTile * kTile;
+  pl.nb = B;
+  pl.nh = Hkv;
+  if (fp8) {
+    const long long one = pl.cap * 4 * kPgD;   // K and V of one kv head of one sequence
+    if (one * Hkv > kWindowBytes) {
+      pl.nb = 1;
+      pl.nh = (int)(kWindowBytes / one < 1 ? 1 : kWindowBytes / one);
+    } else if (one * Hkv * B > kWindowBytes) {
+      pl.nb = (int)(kWindowBytes / (one * Hkv));
+    }
+  }
+  pl.P = pl.nb * pl.nqb;
   return pl;
 }
 
@@ -999,8 +1030,9 @@ constexpr size_t kTcHead = 256;   // the kernel error word
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t tc_part_o_bytes(const TcPlan& pl) { return (size_t)pl.W * 2 * 2 * kTile * kPgD * 4; }
 size_t tc_part_ml_bytes(const TcPlan& pl) { return (size_t)pl.W * 2 * 2 * kTile * 2 * 4; }
-size_t tc_scratch_bytes(const TcPlan& pl) { return (size_t)pl.W * kTile * (kPgD + 4) * 4; }
+size_t tc_scratch_bytes(const TcPlan& pl) { return up256((size_t)pl.W * kTile * (kPgD + 2) * 4); }
 size_t tc_pieces_bytes(const TcPlan& pl) { return up256(pl.W * sizeof(TcPiece)); }
+size_t tc_window_bytes(const TcPlan& pl) { return (size_t)pl.nb * pl.cap * pl.nh * kPgD * 2; }   // K or V
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1032,26 +1064,30 @@ bool make_q_map(CUtensorMap* m, const PagedArgs& a, int tpt) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A pool as [rows][row elements]: box of 128 bytes x a page (at most a tile).
-bool make_pool_map(CUtensorMap* m, const PagedArgs& a, const uint8_t* pool, bool fp8) {
+// K or V as [rows][row elements] (a pool, or a window): box of 64 values x
+// `box_rows` rows.
+bool make_kv_map(CUtensorMap* m, const void* p, long long rows, int row_elems, int row_bytes, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const int rb = paged_row_bytes(fp8, a.Hkv), rows = 1 << a.page_shift;
-  cuuint64_t dims[2] = {(cuuint64_t)(fp8 ? rb : rb / 2), (cuuint64_t)a.num_pages << a.page_shift};
-  cuuint64_t strides[1] = {(cuuint64_t)rb};
-  cuuint32_t box[2] = {fp8 ? 128u : 64u, (cuuint32_t)(rows < kTile ? rows : kTile)};
+  cuuint64_t dims[2] = {(cuuint64_t)row_elems, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(pool),
-            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8>
-cudaError_t launch_tc(const PagedArgs& a, void* ws, cudaStream_t st) {
-  const TcPlan pl = tc_plan(a.B, a.G, a.max_q);
-  CUtensorMap mq, mk, mv;
-  if (!make_q_map(&mq, a, pl.tpt) || !make_pool_map(&mk, a, a.kp, FP8) || !make_pool_map(&mv, a, a.vp, FP8))
-    return cudaErrorInvalidValue;
+}  // namespace
+
+size_t paged_tc_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q, long long capacity) {
+  const TcPlan pl = tc_plan(fp8, B, Hkv, G, max_q, capacity);
+  return kTcHead + tc_pieces_bytes(pl) + tc_part_o_bytes(pl) + tc_part_ml_bytes(pl) + tc_scratch_bytes(pl) +
+         (fp8 ? 2 * up256(tc_window_bytes(pl)) : 0);
+}
+
+cudaError_t launch_paged_tc(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {
+  TcPlan pl = tc_plan(fp8, a.B, a.Hkv, a.G, a.max_q, (long long)a.max_pages << a.page_shift);
   char* p = static_cast<char*>(ws);
   int* err = reinterpret_cast<int*>(p);
   p += kTcHead;
@@ -1062,29 +1098,41 @@ cudaError_t launch_tc(const PagedArgs& a, void* ws, cudaStream_t st) {
   float* pml = reinterpret_cast<float*>(p);
   p += tc_part_ml_bytes(pl);
   float* scratch = reinterpret_cast<float*>(p);
-  auto kern = paged_attn_tc_kernel<FP8>;
-  cudaError_t e = ensure_dynamic_smem((const void*)kern, tc_smem<FP8>());
+  p += tc_scratch_bytes(pl);
+  uint16_t* kw = reinterpret_cast<uint16_t*>(p);
+  uint16_t* vw = reinterpret_cast<uint16_t*>(p + up256(tc_window_bytes(pl)));
+  if (fp8) pl.kw = kw, pl.vw = vw;
+  auto kern = fp8 ? paged_attn_tc_kernel<true> : paged_attn_tc_kernel<false>;
+  cudaError_t e = ensure_dynamic_smem((const void*)kern, kTcSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3((unsigned)pl.W), dim3(kTcThreads), tc_smem<FP8>(), st, mq, mk, mv, a, pl, pieces, po, pml,
-                 scratch, err);
-  if (e != cudaSuccess) return e;
-  if (pl.W > 1) {
-    e = launch_pdl(paged_tc_merge_kernel, dim3((unsigned)(pl.W - 1), 2 * kTile / 32), dim3(256), 0, st, a, pl, pieces,
-                   po, pml, err);
-    if (e != cudaSuccess) return e;
-  }
+  CUtensorMap mq, mk, mv;
+  if (!make_q_map(&mq, a, pl.tpt)) return cudaErrorInvalidValue;
+  const int nb = pl.nb, nh = pl.nh;
+  for (pl.h0 = 0; pl.h0 < a.Hkv; pl.h0 += nh)
+    for (pl.b0 = 0; pl.b0 < a.B; pl.b0 += nb) {
+      pl.nh = nh < a.Hkv - pl.h0 ? nh : a.Hkv - pl.h0;
+      pl.nb = nb < a.B - pl.b0 ? nb : a.B - pl.b0;
+      pl.P = pl.nb * pl.nqb;
+      const int rows = fp8 ? kTile : 1 << a.page_shift, box = rows < kTile ? rows : kTile;
+      const long long n = fp8 ? pl.nb * pl.cap : (long long)a.num_pages << a.page_shift;
+      const int rb = fp8 ? pl.nh * kPgD * 2 : paged_row_bytes(0, a.Hkv);
+      if (!make_kv_map(&mk, fp8 ? (const void*)kw : a.kp, n, rb / 2, rb, box) ||
+          !make_kv_map(&mv, fp8 ? (const void*)vw : a.vp, n, rb / 2, rb, box))
+        return cudaErrorInvalidValue;
+      if (fp8) {
+        e = launch_pdl(paged_window_kernel, dim3((unsigned)(8 * pl.W)), dim3(256), 0, st, a, pl, kw, vw);
+        if (e != cudaSuccess) return e;
+      }
+      e = launch_pdl(kern, dim3((unsigned)pl.W), dim3(kTcThreads), kTcSmem, st, mq, mk, mv, a, pl, pieces, po, pml,
+                     scratch, err);
+      if (e != cudaSuccess) return e;
+      if (pl.W > 1) {
+        e = launch_pdl(paged_tc_merge_kernel, dim3((unsigned)(pl.W - 1), 2 * kTile / 32), dim3(256), 0, st, a, pl,
+                       pieces, po, pml, err);
+        if (e != cudaSuccess) return e;
+      }
+    }
   return cudaGetLastError();
-}
-
-}  // namespace
-
-size_t paged_tc_workspace_bytes(int B, int G, int max_q) {
-  const TcPlan pl = tc_plan(B, G, max_q);
-  return kTcHead + tc_pieces_bytes(pl) + tc_part_o_bytes(pl) + tc_part_ml_bytes(pl) + up256(tc_scratch_bytes(pl));
-}
-
-cudaError_t launch_paged_tc(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {
-  return fp8 ? launch_tc<true>(a, ws, st) : launch_tc<false>(a, ws, st);
 }
 
 }  // namespace sa

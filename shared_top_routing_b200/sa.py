@@ -56,7 +56,7 @@ SIGNATURES = {
     "sa_paged_row_bytes": (_Z, [_I, _I]),
     "sa_paged_kv_write": (_I, [_P, _P, _L, _L, _P, _P, _P] + [_I] * 8 + [_P, _P, _P]),
     "sa_paged_kv_gather": (_I, [_P] * 5 + [_I] * 8 + [_P, _P, _P]),
-    "sa_paged_attn_workspace": (_Z, [_I] * 7),
+    "sa_paged_attn_workspace": (_Z, [_I] * 9),
     "sa_paged_attn": (_I, [_P, _L] + [_P] * 5 + [_I] * 10 + [_F, _P, _P, _P, _Z, _P]),
     "sa_paged_sparse_attn_decode_workspace": (_Z, [_I] * 6),
     "sa_paged_sparse_attn_decode": (_I, [_P] * 6 + [_I] * 9 + [_F, _P, _P, _P, _Z, _P]),
@@ -599,7 +599,8 @@ def sa_paged_attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q: int 
         else:
             _result(out, "out", dev, (N, Hq, D), torch.bfloat16)
         lse = torch.empty((N, Hq), dtype=torch.float32, device=dev) if with_lse else None
-        wp, wn = _paged_ws_args(L.sa_paged_attn_workspace(B, N, max_q, Hq, Hkv, D, kv_type), ws, dev, raw)
+        wp, wn = _paged_ws_args(L.sa_paged_attn_workspace(B, N, max_q, block_table.shape[1], k_pages.shape[1], Hq, Hkv,
+                                                         D, kv_type), ws, dev, raw)
         st = L.sa_paged_attn(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
                              q_start.data_ptr(), kv_len.data_ptr(), B, N, max_q, block_table.shape[1],
                              k_pages.shape[0], k_pages.shape[1], Hq, Hkv, D, kv_type, scale, out.data_ptr(),

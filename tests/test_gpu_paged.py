@@ -547,7 +547,7 @@ def test_error_word_gives_nan(kv_type, q_len):
     pools = [_dev_pool(_random_pool(130 + i, num_pages, page, hkv, kv_type), kv_type) for i in range(2)]
     N = sum(q_len)
     q = to_dev(_normal(20, 1, (N, hkv * G, 128)))
-    need = S.lib().sa_paged_attn_workspace(2, N, max(q_len), hkv * G, hkv, 128, kv_type)
+    need = S.lib().sa_paged_attn_workspace(2, N, max(q_len), table.shape[1], page, hkv * G, hkv, 128, kv_type)
     ws = torch.zeros(need, dtype=torch.uint8, device=dev())
     args = (*pools, i32(table), i32(np.cumsum([0] + q_len)), i32(kv), max(q_len))
     good = sa.sa_paged_attn(q, *args, ws=ws)

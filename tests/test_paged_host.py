@@ -171,16 +171,22 @@ def test_attention_refusals():
 
 def test_workspace_sizes():
     L = S.lib()
-    one = L.sa_paged_attn_workspace(8, 8, 1, 32, 8, 128, S.SA_KV_E4M3)
-    assert 0 < one < 64 << 20
-    assert L.sa_paged_attn_workspace(8, 8, 1, 32, 8, 128, S.SA_KV_BF16) > 0
+    def ws(B=8, N=8, max_q=1, pages=512, page=64, Hq=32, Hkv=8, kv_type=S.SA_KV_E4M3, lib=L):
+        return lib.sa_paged_attn_workspace(B, N, max_q, pages, page, Hq, Hkv, 128, kv_type)
+
+    assert 0 < ws() < 64 << 20 and ws(kv_type=S.SA_KV_BF16) > 0
     # a bound far above the tokens there are asks for no more than the tokens do
-    assert L.sa_paged_attn_workspace(8, 8, 1 << 20, 32, 8, 128, 0) == L.sa_paged_attn_workspace(8, 8, 8, 32, 8, 128, 0)
-    for args in ((0, 1, 1, 32, 8), (1, 0, 1, 32, 8), (1, 1, 0, 32, 8), (1, 1, 1, 32, 9), (1, 1, 1, 33, 8)):
-        assert L.sa_paged_attn_workspace(*args, 128, 0) == 0
+    assert ws(max_q=1 << 20) == ws(max_q=8)
+    for kw in (dict(B=0), dict(N=0), dict(max_q=0), dict(Hkv=9), dict(Hq=33), dict(pages=0), dict(page=0)):
+        assert ws(**kw) == 0
+    # long chunks of E4M3 caches: the rows in bf16, a window of at most 1 GiB at a time
+    long = dict(N=4096, max_q=4096)
+    small = ws(**long, kv_type=S.SA_KV_BF16)
+    assert ws(**long) - small == 8 * 512 * 64 * 8 * 512        # all of 8 x 32K positions, 8 heads
+    assert ws(**long, pages=1 << 14) - small <= 1 << 30        # 8 x 1M positions
+    assert ws(**long, pages=1 << 14) - small > 1 << 28
     assert L.sa_paged_sparse_attn_decode_workspace(8, 32, 8, 128, 2048, 1) > 0
-    assert S.lib_debug().sa_paged_attn_workspace(8, 8, 1, 32, 8, 128, 0) == \
-        L.sa_paged_attn_workspace(8, 8, 1, 32, 8, 128, 0) + 256
+    assert ws(lib=S.lib_debug()) == ws() + 256
 
 
 def test_the_binding_refuses_what_it_cannot_pass_on():
