@@ -139,8 +139,9 @@ __device__ __forceinline__ void read_row(const uint8_t* __restrict__ row, uint16
       uint32_t r[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        r[2 * i] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[i] & 0xffffu), s);
-        r[2 * i + 1] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[i] >> 16), s);
+        e4m3x4_to_f16x4(w[i], r[2 * i], r[2 * i + 1]);
+        r[2 * i] = f16x2_to_bf16x2(r[2 * i], s);
+        r[2 * i + 1] = f16x2_to_bf16x2(r[2 * i + 1], s);
       }
       uint4* d = reinterpret_cast<uint4*>(dst + h * kPgD + j * 16);
       d[0] = make_uint4(r[0], r[1], r[2], r[3]);
@@ -194,9 +195,15 @@ constexpr int kRwConsumers = 8;
 constexpr int kRwThreads = (kRwConsumers + 1) * 32;
 constexpr int kRwMaxStages = 8;
 constexpr int kRwBarBytes = 256;       // mbarriers, abort word, plan
-constexpr int kRwStageBytes = 208 * 1024;
+constexpr int kRwStageBytes = 222 * 1024;
 constexpr int kRwMergeThreads = 256;
 constexpr int kRwMergeMaxC = 1280;     // contributors of one (row block, head)
+
+// Positions a consumer warp takes per step: codes are half the bytes, so twice
+// as many for the same stage, with more independent products in flight (16:
+// 184 us for one token of each of 8 x 32K positions, 8 kv heads).
+template <bool FP8>
+constexpr int kRwKeys = FP8 ? 32 : 16;
 
 struct RowsPlan {
   int nrb, tb, RB;         // row blocks per sequence, tokens and rows of one
@@ -309,9 +316,9 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
 }
 
 // Running state of one warp's 16 rows: output, its reference (base-2
-// logarithm), softmax maximum and sum.  For codes the output's reference mo
-// bounds z + log2(scale of v), so the weights that multiply the codes stay
-// within fp16; for bf16 it is the maximum itself.
+// logarithm), the softmax's reference and sum.  For codes the output's
+// reference mo bounds z + log2(scale of v), so the weights that multiply the
+// codes stay within fp16; for bf16 one reference serves both.
 struct RowState {
   float o[16][4];
   float m[2], l[2], mo[2];
@@ -337,49 +344,60 @@ __device__ __forceinline__ uint32_t clean_halves(uint32_t v, uint32_t ex, bool& 
   return keep_halves(v, !lo, !hi);
 }
 
-// Weights are at most 2^15, so fp16 keeps what is within 2^-39 of the
-// largest weight of its row.
-constexpr float kRwLift = 15.f;
+// A reference rises only when a logit exceeds it by more than 2^kRwLazy, so
+// the output is seldom scaled.  fp16 weights are at most 2^(kRwLift + kRwLazy)
+// = 2^15 and keep what is within 2^-33 of the largest weight of their row.
+constexpr float kRwLift = 9.f, kRwLazy = 6.f;
 
-// One step over a 16-position slice of a tile: scores, running maximum and
+// One step over a slice of a tile (KS positions): scores, running maximum and
 // sum, output.  tK, tV: the slice's first row, this kv head; rb: bytes from
 // row to row; sK, sV: the scale bytes of this head in the slice's first row.
 // Key rbase + i is seen by row r when it is <= lim[r] (-1: never).
-// edge: some key of the slice is not seen by some row.  Then V rows that no
+// EDGE: some key of the slice is not seen by some row.  Then V rows that no
 // row sees are zeroed, and infinities and NaN in V are taken out of the
 // product and added to the rows that see them only.
-template <bool FP8>
+template <bool FP8, bool EDGE>
 __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4], const float (&rowc)[2],
                                          const uint8_t* tK, const uint8_t* tV, int rb, const uint8_t* sK,
-                                         const uint8_t* sV, int rbase, const int (&lim)[2], int top, bool edge) {
+                                         const uint8_t* sV, int rbase, const int (&lim)[2], int top) {
+  constexpr int KS = kRwKeys<FP8>, NT = KS / 8;
   const int lane = threadIdx.x & 31, tg = lane & 3, mtx = lane >> 3;
-  float sc[2][4], sd[2][4];
+  float sc[NT][4];
 #pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sc[nt][e] = sd[nt][e] = 0.f;
-  float kscale[2][2], vexp[2][2];
+    for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+  float kscale[NT][2], vexp[NT][2];
   if constexpr (FP8) {
     const uint8_t* kr = tK + ((mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
 #pragma unroll
-    for (int c = 0; c < 8; c += 2) {   // 16 keys x 32 codes
-      uint32_t w[4];                   // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
-      ldmatrix_x4(w[0], w[1], w[2], w[3], kr + c * 16);
+    for (int c = 0; c < 8; c += 2) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        mma_f16_16816(sc[nt], qa[c], e4m3x2_to_f16x2(w[nt] & 0xffffu), e4m3x2_to_f16x2(w[nt] >> 16));
-        mma_f16_16816(sd[nt], qa[c + 1], e4m3x2_to_f16x2(w[2 + nt] & 0xffffu), e4m3x2_to_f16x2(w[2 + nt] >> 16));
+      for (int kh = 0; kh < KS / 16; ++kh) {   // 16 keys x 32 codes
+        uint32_t w[4];                         // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
+        ldmatrix_x4(w[0], w[1], w[2], w[3], kr + kh * 16 * rb + c * 16);
+        uint32_t b[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], b[i][0], b[i][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_f16_16816(sc[2 * kh + (i & 1)], qa[c + (i >> 1)], b[i][0], b[i][1]);
       }
     }
+    // lane l converts the scales of key l; each lane takes those of its keys
+    const float ks = e8m0_value(sK[lane * rb]), ve = e8m0_exponent(sV[lane * rb]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        kscale[nt][e] = __shfl_sync(0xffffffffu, ks, nt * 8 + tg * 2 + e);
+        vexp[nt][e] = __shfl_sync(0xffffffffu, ve, nt * 8 + tg * 2 + e);
+      }
+  } else {
+    float sd[2][4];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = nt * 8 + tg * 2 + e;
-        kscale[nt][e] = e8m0_value(sK[row * rb]);
-        vexp[nt][e] = e8m0_exponent(sV[row * rb]);
-      }
-  } else {
+      for (int e = 0; e < 4; ++e) sd[nt][e] = 0.f;
     const uint8_t* kr = tK + ((mtx >> 1) * 8 + (lane & 7)) * rb + (mtx & 1) * 16;
 #pragma unroll
     for (int kk = 0; kk < 8; kk += 2) {
@@ -391,45 +409,45 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
       mma_bf16_16816(sd[0], qa[kk + 1], c0, c1);
       mma_bf16_16816(sd[1], qa[kk + 1], c2, c3);
     }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[nt][e] += sd[nt][e];
   }
   // base-2 logits; masked ones are -inf whatever the product was
   float mx[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
-  float zo[2][4];   // z + log2(scale of v)
 #pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int hh = e >> 1, key = rbase + nt * 8 + tg * 2 + (e & 1);
-      float z = (sc[nt][e] + sd[nt][e]) * rowc[hh];
+      const int hh = e >> 1;
+      float z = sc[nt][e] * rowc[hh];
       if constexpr (FP8) z *= kscale[nt][e & 1];
-      z = key <= lim[hh] ? z : -INFINITY;
+      if (EDGE) z = rbase + nt * 8 + tg * 2 + (e & 1) <= lim[hh] ? z : -INFINITY;
       sc[nt][e] = z;
       mx[hh] = fmaxf(mx[hh], z);
-      if constexpr (FP8) {
-        zo[nt][e] = key <= lim[hh] ? z + vexp[nt][e & 1] : -INFINITY;
-        mv[hh] = fmaxf(mv[hh], zo[nt][e]);
-      }
+      // (an exponent that is NaN makes the weight NaN, not the reference)
+      if constexpr (FP8) mv[hh] = fmaxf(mv[hh], z + vexp[nt][e & 1]);
     }
-  float alpha[2];
+  float alpha[2], muse[2];
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
     float v = mx[hh];
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-    const float mnew = fmaxf(st.m[hh], v);
-    const float muse = mnew == -INFINITY ? 0.f : mnew;
-    alpha[hh] = exp2f(st.m[hh] - muse);
+    const float mnew = v > st.m[hh] + kRwLazy ? v : st.m[hh];
+    muse[hh] = mnew == -INFINITY ? 0.f : mnew;
+    alpha[hh] = mnew == st.m[hh] ? 1.f : ex2(st.m[hh] - muse[hh]);
     st.m[hh] = mnew;
-    mx[hh] = muse;
   }
   float rsum[2] = {0.f, 0.f};
+  float wt[NT][4];   // the weights that multiply V
 #pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float pv = exp2f(sc[nt][e] - mx[e >> 1]);
-      sc[nt][e] = pv;
-      rsum[e >> 1] += pv;
+      wt[nt][e] = ex2(sc[nt][e] - muse[e >> 1]);
+      rsum[e >> 1] += wt[nt][e];
     }
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
@@ -444,16 +462,20 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
       float v = mv[hh];
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-      const float mnew = fmaxf(st.mo[hh], v);
-      const float muse = mnew == -INFINITY ? 0.f : mnew;
-      alpha[hh] = exp2f(st.mo[hh] - muse);
+      const float mnew = v > st.mo[hh] + kRwLazy ? v : st.mo[hh];
+      const float mu = mnew == -INFINITY ? 0.f : mnew;
+      alpha[hh] = mnew == st.mo[hh] ? 1.f : ex2(st.mo[hh] - mu);
       st.mo[hh] = mnew;
-      mv[hh] = muse - kRwLift;
+      mv[hh] = mu - kRwLift;
     }
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][e] = exp2f(zo[nt][e] - mv[e >> 1]);
+      for (int e = 0; e < 4; ++e) {
+        float zo = sc[nt][e] + vexp[nt][e & 1];
+        if (EDGE) zo = sc[nt][e] == -INFINITY ? -INFINITY : zo;   // (a masked row's scale may be NaN)
+        wt[nt][e] = ex2(zo - mv[e >> 1]);
+      }
   }
   if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {   // a reference moved
 #pragma unroll
@@ -465,66 +487,68 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
     }
   }
   bool bad = false;
-  // V fragment registers hold keys 2 tg, 2 tg + 1 (b0) and those + 8 (b1)
-  const int k0 = rbase + 2 * tg;
-  if constexpr (FP8) {
-    uint32_t pa[4] = {pack_f16x2(sc[0][0], sc[0][1]), pack_f16x2(sc[0][2], sc[0][3]),
-                      pack_f16x2(sc[1][0], sc[1][1]), pack_f16x2(sc[1][2], sc[1][3])};
-    const uint8_t* vr = tV + ((mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
 #pragma unroll
-    for (int c = 0; c < 8; c += 2) {
-      uint32_t w[4];   // transposed: keys 2 tg, 2 tg + 1 x codes 2 gq, 2 gq + 1 of a chunk
-      ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vr + c * 16);
+  for (int kh = 0; kh < KS / 16; ++kh) {
+    // V fragment registers hold keys 2 tg, 2 tg + 1 (b0) and those + 8 (b1)
+    const int k0 = rbase + kh * 16 + 2 * tg;
+    const uint8_t* vr = tV + (kh * 16 + (mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
+    const float(&u)[4] = wt[2 * kh], (&v)[4] = wt[2 * kh + 1];
+    if constexpr (FP8) {
+      uint32_t pa[4] = {pack_f16x2(u[0], u[1]), pack_f16x2(u[2], u[3]), pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t x0 = __byte_perm(w[2 * i], 0u, 0x3120), x1 = __byte_perm(w[2 * i + 1], 0u, 0x3120);
-        uint32_t b[4] = {e4m3x2_to_f16x2(x0 & 0xffffu), e4m3x2_to_f16x2(x1 & 0xffffu), e4m3x2_to_f16x2(x0 >> 16),
-                         e4m3x2_to_f16x2(x1 >> 16)};
-        if (edge) {
+      for (int c = 0; c < 8; c += 2) {
+        uint32_t w[4];   // transposed: keys 2 tg, 2 tg + 1 x codes 2 gq, 2 gq + 1 of a chunk
+        ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vr + c * 16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t b[4];   // even codes of keys 0-7 and 8-15, then odd ones
+          e4m3x4_to_f16x4(__byte_perm(w[2 * i], 0u, 0x3120), b[0], b[2]);
+          e4m3x4_to_f16x4(__byte_perm(w[2 * i + 1], 0u, 0x3120), b[1], b[3]);
+          if (EDGE) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const int kb = k0 + (h & 1) * 8;
+              b[h] = clean_halves(keep_halves(b[h], kb <= top, kb + 1 <= top), 0x7c00u, bad);
+            }
+          }
+          mma_f16_16816(st.o[2 * (c + i)], pa, b[0], b[1]);
+          mma_f16_16816(st.o[2 * (c + i) + 1], pa, b[2], b[3]);
+        }
+      }
+    } else {
+      uint32_t pa[4] = {pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]),
+                        pack_bf16x2(v[2], v[3])};
+#pragma unroll
+      for (int dt = 0; dt < 16; dt += 2) {
+        uint32_t b[4];
+        ldmatrix_x4_trans(b[0], b[1], b[2], b[3], vr + dt * 16);
+        if (EDGE) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const int kb = k0 + (h & 1) * 8;
-            b[h] = clean_halves(keep_halves(b[h], kb <= top, kb + 1 <= top), 0x7c00u, bad);
+            b[h] = clean_halves(keep_halves(b[h], kb <= top, kb + 1 <= top), 0x7f80u, bad);
           }
         }
-        mma_f16_16816(st.o[2 * (c + i)], pa, b[0], b[1]);
-        mma_f16_16816(st.o[2 * (c + i) + 1], pa, b[2], b[3]);
+        mma_bf16_16816(st.o[dt], pa, b[0], b[1]);
+        mma_bf16_16816(st.o[dt + 1], pa, b[2], b[3]);
       }
-    }
-  } else {
-    uint32_t pa[4] = {pack_bf16x2(sc[0][0], sc[0][1]), pack_bf16x2(sc[0][2], sc[0][3]),
-                      pack_bf16x2(sc[1][0], sc[1][1]), pack_bf16x2(sc[1][2], sc[1][3])};
-    const uint8_t* vr = tV + ((mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
-#pragma unroll
-    for (int dt = 0; dt < 16; dt += 2) {
-      uint32_t b[4];
-      ldmatrix_x4_trans(b[0], b[1], b[2], b[3], vr + dt * 16);
-      if (edge) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int kb = k0 + (h & 1) * 8;
-          b[h] = clean_halves(keep_halves(b[h], kb <= top, kb + 1 <= top), 0x7f80u, bad);
-        }
-      }
-      mma_bf16_16816(st.o[dt], pa, b[0], b[1]);
-      mma_bf16_16816(st.o[dt + 1], pa, b[2], b[3]);
     }
   }
-  if (edge && __any_sync(0xffffffffu, bad)) {
+  if (EDGE && __any_sync(0xffffffffu, bad)) {
     // rare: infinities and NaN of V reach the rows that see their key
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < KS; ++i) {
       if (rbase + i > top) break;
       const uint8_t* row = tV + (size_t)i * rb;
 #pragma unroll
       for (int dt = 0; dt < 16; ++dt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // column of st.o[dt][e]: see flush_rows
+          // column of st.o[dt][e]: see the partials' stores
           const int d = FP8 ? (dt >> 1) * 16 + 4 * tg + 2 * (e & 1) + (dt & 1) : dt * 8 + 2 * tg + (e & 1);
-          float v;
-          if constexpr (FP8) v = (row[d] & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
-          else v = bf_lo(reinterpret_cast<const uint16_t*>(row)[d]);
-          if (!isfinite(v) && rbase + i <= lim[e >> 1]) st.o[dt][e] += v;
+          float x;
+          if constexpr (FP8) x = (row[d] & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
+          else x = bf_lo(reinterpret_cast<const uint16_t*>(row)[d]);
+          if (!isfinite(x) && rbase + i <= lim[e >> 1]) st.o[dt][e] += x;
         }
     }
   }
@@ -601,11 +625,12 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
       // tile's copies are issued
       int e0 = 0, pg = 0, pg_next = 0;
       const int e_last = SPARSE ? 0 : (keys - 1) >> a.page_shift;
-      int jn[4] = {0, 0, 0, 0}, pn[4] = {0, 0, 0, 0}, jnn[4] = {0, 0, 0, 0};
+      constexpr int NI = kRwKeys<FP8> / 4;   // rows per lane: a tile has at most 8 slices
+      int jn[NI] = {}, pn[NI] = {}, jnn[NI] = {};
       const int32_t* irow = SPARSE ? a.idx + (long long)b * a.k : nullptr;
-      auto load_idx = [&](int (&j)[4], int t) {
+      auto load_idx = [&](int (&j)[NI], int t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NI; ++i) {
           const int r = lane + 32 * i, at = t * R + r;
           if (r < R && at < keys) {
             int v = __ldg(irow + at);
@@ -617,9 +642,9 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
           }
         }
       };
-      auto load_pages = [&](int (&g)[4], const int (&j)[4], int t) {
+      auto load_pages = [&](int (&g)[NI], const int (&j)[NI], int t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NI; ++i) {
           const int r = lane + 32 * i;
           if (r < R && t * R + r < keys) g[i] = __ldg(trow + (j[i] >> a.page_shift));
         }
@@ -646,13 +671,13 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
         if (lane == 0) tc::mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)rows * (uint32_t)rb);
         __syncwarp();
         if constexpr (SPARSE) {
-          int jc[4], pc[4];
+          int jc[NI], pc[NI];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) jc[i] = jn[i], pc[i] = pn[i], jn[i] = jnn[i];
+          for (int i = 0; i < NI; ++i) jc[i] = jn[i], pc[i] = pn[i], jn[i] = jnn[i];
           if (t + 1 < last) load_pages(pn, jn, t + 1);
           if (t + 2 < last) load_idx(jnn, t + 2);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < NI; ++i) {
             const int r = lane + 32 * i;
             if (r < rows) {
               const int page = checked_page(pc[i], a.num_pages, a.dbg);
@@ -732,13 +757,15 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
         ok = false;
         break;
       }
-      const int rbase = t * R + rs * 16;
+      const int rbase = t * R + rs * kRwKeys<FP8>;
       if (active && rbase < keys) {
-        const uint8_t* tK = ring + (size_t)s * stage_bytes + (size_t)(rs * 16) * rb;
+        const uint8_t* tK = ring + (size_t)s * stage_bytes + (size_t)(rs * kRwKeys<FP8>) * rb;
         const uint8_t* tV = tK + (size_t)R * rb;
         const int tail = a.Hkv * kPgD + hs, off = hs * (FP8 ? kPgD : 2 * kPgD);
-        row_step<FP8>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1,
-                      rbase + 15 > low);
+        if (rbase + kRwKeys<FP8> - 1 > low)
+          row_step<FP8, true>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
+        else
+          row_step<FP8, false>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&empty[s]);
@@ -912,7 +939,7 @@ RowsPlan rows_plan(int fp8, int B, int Hkv, int G, int max_q) {
   pl.RB = pl.tb * G;
   pl.P = B * pl.nrb;
   pl.wph = kRwConsumers / Hkv;   // 8, 4, 2 or 1 for Hkv <= 8: tiles and pages are powers of two, neither
-  pl.R = 16 * pl.wph;            // straddles the other
+  pl.R = (fp8 ? kRwKeys<true> : kRwKeys<false>) * pl.wph;   // straddles the other
   pl.row_bytes = paged_row_bytes(fp8, Hkv);
   const int stage = 2 * pl.R * pl.row_bytes;
   pl.stages = kRwStageBytes / stage < kRwMaxStages ? kRwStageBytes / stage : kRwMaxStages;

@@ -72,11 +72,11 @@ __device__ __forceinline__ float e8m0_exponent(uint32_t b) {
   return b == 255u ? __uint_as_float(0x7fc00000u) : (float)(int)b - 127.f;
 }
 
-// Two E4M3 codes (low byte first) -> two fp16 values, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t lo16) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(lo16));
-  return r;
+// Four E4M3 codes (low byte first) -> four fp16 values in two words, exact.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 // Two fp16 values -> two bf16 values times `s` (each product rounded once).
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h, float s) {
@@ -86,6 +86,12 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h, float s) {
       : "r"(h));
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b * s), "f"(a * s));
+  return r;
+}
+// 2^x (results below 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {

@@ -197,11 +197,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 // Two fp32 operations in one instruction (sm_100).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -910,8 +905,9 @@ paged_window_kernel(const PagedArgs a, const TcPlan pl, uint16_t* __restrict__ k
           uint32_t r[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            r[2 * i] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[i] & 0xffffu), sc);
-            r[2 * i + 1] = f16x2_to_bf16x2(e4m3x2_to_f16x2(w[i] >> 16), sc);
+            e4m3x4_to_f16x4(w[i], r[2 * i], r[2 * i + 1]);
+            r[2 * i] = f16x2_to_bf16x2(r[2 * i], sc);
+            r[2 * i + 1] = f16x2_to_bf16x2(r[2 * i + 1], sc);
           }
           uint4* d = reinterpret_cast<uint4*>(dst + h * kPgD + j * 16);
           d[0] = make_uint4(r[0], r[1], r[2], r[3]);
