@@ -802,12 +802,14 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
 
 // One CTA per (token, query head): out = sum_x w_x o_x / L, w_x = 2^(m_x - M),
 // L = sum_x w_x l_x, M = max_x m_x over the contributors x of its row block.
+// (64 registers a thread, so that it is resident beside the kernel before and
+// has its place in the list worked out when that ends.)
 template <bool SPARSE>
-__global__ void __launch_bounds__(kRwMergeThreads)
+__global__ void __launch_bounds__(kRwMergeThreads, 4)
 paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* __restrict__ part_o,
                              const float* __restrict__ part_ml, const int* __restrict__ err) {
   constexpr int kWarps = kRwMergeThreads / 32;
-  constexpr int kPre = 16;
+  constexpr int kPre = 8;
   __shared__ float wts[kRwMergeMaxC];
   __shared__ float red[kWarps][kPgD];
   __shared__ float rmax[kWarps], rsum[kWarps];

@@ -425,85 +425,118 @@ def sa_paged_kv_alloc(num_pages: int, page_size: int, Hkv: int, kv_type: int = S
     return tuple(torch.zeros((num_pages, page_size, row), dtype=dtype, device=device) for _ in range(2))
 
 
+# The checks below run on every call of a decode step, so they are written for
+# few interpreter steps: devices as ordinals, one tuple comparison per shape.
+
 def _pools(k_pages, v_pages, dev):
-    """(kv_type, Hkv) of a pair of pools: by their element type and row size."""
+    """(kv_type, Hkv) of a pair of pools on CUDA device `dev` (an ordinal): by
+    their element type and row size."""
     torch = _torch()
-    if k_pages.dtype not in (torch.bfloat16, torch.uint8):
+    dtype, shape = k_pages.dtype, k_pages.shape
+    if dtype is torch.bfloat16:
+        kv_type, pad = SA_KV_BF16, 8
+    elif dtype is torch.uint8:
+        kv_type, pad = SA_KV_E4M3, 16
+    else:
         raise ValueError("k_pages must be bfloat16, or uint8 for E4M3 rows")
-    if k_pages.dim() != 3 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+    if len(shape) != 3 or v_pages.shape != shape or v_pages.dtype is not dtype:
         raise ValueError("k_pages and v_pages must be pools [num_pages, page_size, row] of one shape and type")
-    kv_type = SA_KV_BF16 if k_pages.dtype == torch.bfloat16 else SA_KV_E4M3
-    Hkv, rest = divmod(k_pages.shape[2] - (8 if kv_type == SA_KV_BF16 else 16), _D)
+    Hkv, rest = divmod(shape[2] - pad, _D)
     if rest or Hkv < 1:
-        raise ValueError(f"rows of {k_pages.shape[2]} elements are not a paged cache's (see sa.h)")
-    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if t.device != dev:
-            raise ValueError(f"{n} must be on {dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
+        raise ValueError(f"rows of {shape[2]} elements are not a paged cache's (see sa.h)")
+    if k_pages.get_device() != dev or v_pages.get_device() != dev:
+        raise ValueError(f"k_pages and v_pages must be on {_name(dev)}")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("k_pages and v_pages must be contiguous")
     return kv_type, Hkv
 
 
+def _name(dev):
+    return "the CPU" if dev < 0 else f"cuda:{dev}"
+
+
 def _ints32(t, name, dev, shape):
-    if t.dtype != _torch().int32 or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
-    if tuple(t.shape) != shape:
+    if t.dtype is not _torch().int32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on {_name(dev)}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, has {list(t.shape)}")
 
 
-def _tokens(t, name, dev):
-    """Token stride of [N, H, 128] bf16 rows whose heads lie side by side."""
-    if t.dtype != _torch().bfloat16 or not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} must be a bfloat16 CUDA tensor on {dev}")
-    if t.dim() != 3:
+def _tokens(t, name):
+    """(device ordinal, shape, token stride) of [N, H, 128] bf16 rows whose
+    heads lie side by side."""
+    dev = t.get_device()
+    if dev < 0 or t.dtype is not _torch().bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must have shape [N, heads, {_D}]")
-    H = t.shape[1]
-    if t.shape[2] > 1 and t.stride(2) != 1 or H > 1 and t.stride(1) != t.shape[2]:
+    N, H, D = shape
+    st = t.stride()
+    if D > 1 and st[2] != 1 or H > 1 and st[1] != D:
         raise ValueError(f"{name}'s heads must lie side by side in a token")
-    return t.stride(0) if t.shape[0] > 1 else max(8, H * t.shape[2])
+    return dev, shape, st[0] if N > 1 else max(8, H * D)
 
 
 def _result(t, name, dev, shape, dtype):
     """An output buffer the caller gave, checked."""
-    if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {dev}")
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {_name(dev)}")
+    return t
 
 
 def _call_stream(dev, stream):
-    """(raw stream, context) a call on tensors of `dev` runs on: the given
-    stream, or the current one of that device; the context makes the device
-    (and a given stream, so that outputs belong to it) current."""
-    import contextlib
+    """(raw stream, context or None) a call on tensors of device `dev` runs on:
+    the given stream, or the current one of that device.  The context makes
+    the device (and a given stream, so that outputs belong to it) current;
+    None when they are already."""
     torch = _torch()
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"the stream is of {stream.device}, the tensors are on {dev}")
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is of {stream.device}, the tensors are on {_name(dev)}")
         return stream.cuda_stream, torch.cuda.stream(stream)
-    raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch.cuda.current_device() != dev.index:
-        return raw, torch.cuda.device(dev)
-    return raw, contextlib.nullcontext()
+    raw = torch._C._cuda_getCurrentRawStream(dev)
+    return raw, None if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
 
 
 _paged_ws: dict = {}
+_paged_ws_need: dict = {}
 
 
-def _paged_workspace(nbytes: int, dev, raw_stream: int):
-    """A workspace for one call on a stream (whose context is current).
-    Outside a capture, one buffer per stream is kept and grows.  A capture
-    gets a buffer of its own from the graph's memory, zeroed by the graph, so
-    that graphs share none with each other or with calls outside."""
+def _paged_workspace(nbytes: int, dev: int, raw_stream: int):
+    """A workspace for one call on a stream (whose device is current).  Outside
+    a capture, one buffer per stream is kept and grows.  A capture gets a
+    buffer of its own from the graph's memory, zeroed by the graph, so that
+    graphs share none with each other or with calls outside."""
     torch = _torch()
-    if torch.cuda.is_current_stream_capturing():
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
         buf[:SA_WS_ALIGN].zero_()
         return buf
-    key = (dev.index, raw_stream)
+    key = (dev, raw_stream)
     buf = _paged_ws.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        buf = torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
         _paged_ws[key] = buf
     return buf
+
+
+def _paged_ws_args(L, size_of, sizes, ws, dev, raw):
+    """(pointer, bytes) of the call's workspace; its size is a function of the
+    call's sizes alone and is looked up once."""
+    key = (L._handle, dev, size_of, sizes)
+    need = _paged_ws_need.get(key)
+    if need is None:
+        if len(_paged_ws_need) > 4096:   # (a server meets new sizes for ever)
+            _paged_ws_need.clear()
+        need = _paged_ws_need[key] = getattr(L, size_of)(*sizes)
+    if ws is None:
+        if need == 0:
+            return None, 0
+        ws = _paged_workspace(need, dev, raw)
+    elif ws.get_device() != dev:
+        raise ValueError(f"ws must be on {_name(dev)}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def sa_paged_kv_write(k_new, v_new, k_pages, v_pages, block_table, q_start, kv_len, stream=None):
@@ -512,63 +545,86 @@ def sa_paged_kv_write(k_new, v_new, k_pages, v_pages, block_table, q_start, kv_l
     k_new, v_new [N, Hkv, 128] bf16 (slices of a fused projection are fine);
     pools from sa_paged_kv_alloc; block_table [B, max_pages], q_start [B + 1],
     kv_len [B] int32, kv_len counting the new tokens.  Returns the pools."""
-    dev = k_new.device
-    ks, vs = _tokens(k_new, "k_new", dev), _tokens(v_new, "v_new", dev)
+    dev, kshape, ks = _tokens(k_new, "k_new")
+    vdev, vshape, vs = _tokens(v_new, "v_new")
     kv_type, Hkv = _pools(k_pages, v_pages, dev)
-    N, B = k_new.shape[0], kv_len.shape[0]
-    if k_new.shape != (N, Hkv, _D) or v_new.shape != (N, Hkv, _D):
-        raise ValueError(f"k_new and v_new must have shape [N, {Hkv}, {_D}]")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have shape [B, max_pages]")
-    _ints32(block_table, "block_table", dev, (B, block_table.shape[1]))
+    N = kshape[0]
+    if kshape != (N, Hkv, _D) or vshape != kshape or vdev != dev:
+        raise ValueError(f"k_new and v_new must have shape [N, {Hkv}, {_D}], on one device")
+    B, cols = _table(block_table, dev)
     _ints32(q_start, "q_start", dev, (B + 1,))
     _ints32(kv_len, "kv_len", dev, (B,))
     raw, ctx = _call_stream(dev, stream)
-    with ctx:
-        st = lib().sa_paged_kv_write(k_new.data_ptr(), v_new.data_ptr(), ks, vs, q_start.data_ptr(),
-                                     kv_len.data_ptr(), block_table.data_ptr(), B, N, block_table.shape[1],
-                                     k_pages.shape[0], k_pages.shape[1], Hkv, _D, kv_type, k_pages.data_ptr(),
-                                     v_pages.data_ptr(), raw)
+    pages, page_size, _ = k_pages.shape
+    args = (k_new.data_ptr(), v_new.data_ptr(), ks, vs, q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), B,
+            N, cols, pages, page_size, Hkv, _D, kv_type, k_pages.data_ptr(), v_pages.data_ptr(), raw)
+    if ctx is None:
+        st = lib().sa_paged_kv_write(*args)
+    else:
+        with ctx:
+            st = lib().sa_paged_kv_write(*args)
     _check(st, "sa_paged_kv_write")
     return k_pages, v_pages
+
+
+def _table(block_table, dev):
+    """(sequences, columns) of a block table."""
+    shape = block_table.shape
+    if len(shape) != 2:
+        raise ValueError("block_table must have shape [B, max_pages]")
+    _ints32(block_table, "block_table", dev, shape)
+    return shape
+
+
+def _selection(idx, count, B, dev):
+    """k of a selection idx [B, k], count [B]."""
+    if idx.dim() != 2:
+        raise ValueError("idx must have shape [B, k]")
+    k = idx.shape[1]
+    _ints32(idx, "idx", dev, (B, k))
+    _ints32(count, "count", dev, (B,))
+    return k
 
 
 def sa_paged_kv_gather(k_pages, v_pages, block_table, idx, count, k_rows=None, v_rows=None, stream=None):
     """Selected rows of a paged cache as compact bf16 rows [B, k, Hkv * 128 + 8]
     (zeros past count), for sa_sparse_attn_decode_rows.  idx [B, k], count [B]."""
-    torch = _torch()
-    dev = k_pages.device
+    dev = k_pages.get_device()
     kv_type, Hkv = _pools(k_pages, v_pages, dev)
-    if idx.dim() != 2 or block_table.dim() != 2:
-        raise ValueError("idx must have shape [B, k] and block_table [B, max_pages]")
-    B, k = idx.shape
-    _ints32(block_table, "block_table", dev, (B, block_table.shape[1]))
-    _ints32(idx, "idx", dev, (B, k))
-    _ints32(count, "count", dev, (B,))
-    shape = (B, k, Hkv * _D + 8)
+    B, cols = _table(block_table, dev)
+    k = _selection(idx, count, B, dev)
+    if dev < 0:
+        raise ValueError("k_pages must be a CUDA tensor")
     raw, ctx = _call_stream(dev, stream)
-    with ctx:
-        if k_rows is None:
-            k_rows = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        else:
-            _result(k_rows, "k_rows", dev, shape, torch.bfloat16)
-        if v_rows is None:
-            v_rows = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        else:
-            _result(v_rows, "v_rows", dev, shape, torch.bfloat16)
-        st = lib().sa_paged_kv_gather(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), idx.data_ptr(),
-                                      count.data_ptr(), B, block_table.shape[1], k_pages.shape[0], k_pages.shape[1],
-                                      Hkv, _D, k, kv_type, k_rows.data_ptr(), v_rows.data_ptr(), raw)
+    if ctx is not None:
+        with ctx:
+            return _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, Hkv, B, cols, k, dev, raw)
+    return _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, Hkv, B, cols, k, dev, raw)
+
+
+def _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, Hkv, B, cols, k, dev, raw):
+    bf16 = _torch().bfloat16
+    shape = (B, k, Hkv * _D + 8)
+    k_rows = k_pages.new_empty(shape, dtype=bf16) if k_rows is None else _result(k_rows, "k_rows", dev, shape, bf16)
+    v_rows = k_pages.new_empty(shape, dtype=bf16) if v_rows is None else _result(v_rows, "v_rows", dev, shape, bf16)
+    pages, page_size, _ = k_pages.shape
+    st = lib().sa_paged_kv_gather(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), idx.data_ptr(),
+                                  count.data_ptr(), B, cols, pages, page_size, Hkv, _D, k, kv_type, k_rows.data_ptr(),
+                                  v_rows.data_ptr(), raw)
     _check(st, "sa_paged_kv_gather")
     return k_rows, v_rows
 
 
-def _paged_ws_args(need, ws, dev, raw):
-    if ws is None:
-        ws = _paged_workspace(need, dev, raw) if need else None
-    elif ws.device != dev:
-        raise ValueError(f"ws must be on {dev}")
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _outputs(q, shape, out, with_lse, dev):
+    """(out, lse or None) of queries q [N, Hq, 128]."""
+    torch = _torch()
+    if out is not None:
+        _result(out, "out", dev, shape, torch.bfloat16)
+    elif q.is_contiguous():
+        out = torch.empty_like(q)
+    else:
+        out = q.new_empty(shape)
+    return out, q.new_empty(shape[:2], dtype=torch.float32) if with_lse else None
 
 
 def sa_paged_attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q: int | None = None, scale: float = 0.0,
@@ -579,32 +635,32 @@ def sa_paged_attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q: int 
     q [N, Hq, 128] bf16, the sequences' tokens packed by q_start [B + 1];
     kv_len [B] counts them; max_q bounds the tokens of one sequence (1 for
     decode; by default N).  Returns out [N, Hq, 128][, lse [N, Hq] fp32]."""
-    torch = _torch()
-    dev = q.device
-    qs = _tokens(q, "q", dev)
+    dev, shape, qs = _tokens(q, "q")
     kv_type, Hkv = _pools(k_pages, v_pages, dev)
-    N, Hq, D = q.shape
-    B = kv_len.shape[0]
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have shape [B, max_pages]")
-    _ints32(block_table, "block_table", dev, (B, block_table.shape[1]))
+    B, cols = _table(block_table, dev)
     _ints32(q_start, "q_start", dev, (B + 1,))
     _ints32(kv_len, "kv_len", dev, (B,))
-    max_q = N if max_q is None else max_q
     raw, ctx = _call_stream(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return _attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q, scale, out, with_lse, ws, dev, shape,
+                         qs, kv_type, Hkv, B, cols, raw)
+    return _attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q, scale, out, with_lse, ws, dev, shape, qs,
+                 kv_type, Hkv, B, cols, raw)
+
+
+def _attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q, scale, out, with_lse, ws, dev, shape, qs, kv_type,
+          Hkv, B, cols, raw):
     L = lib()
-    with ctx:
-        if out is None:
-            out = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=dev)
-        else:
-            _result(out, "out", dev, (N, Hq, D), torch.bfloat16)
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev) if with_lse else None
-        wp, wn = _paged_ws_args(L.sa_paged_attn_workspace(B, N, max_q, block_table.shape[1], k_pages.shape[1], Hq, Hkv,
-                                                         D, kv_type), ws, dev, raw)
-        st = L.sa_paged_attn(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-                             q_start.data_ptr(), kv_len.data_ptr(), B, N, max_q, block_table.shape[1],
-                             k_pages.shape[0], k_pages.shape[1], Hq, Hkv, D, kv_type, scale, out.data_ptr(),
-                             None if lse is None else lse.data_ptr(), wp, wn, raw)
+    N, Hq, D = shape
+    max_q = N if max_q is None else max_q
+    out, lse = _outputs(q, shape, out, with_lse, dev)
+    pages, page_size, _ = k_pages.shape
+    wp, wn = _paged_ws_args(L, "sa_paged_attn_workspace", (B, N, max_q, cols, page_size, Hq, Hkv, D, kv_type), ws, dev,
+                            raw)
+    st = L.sa_paged_attn(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                         q_start.data_ptr(), kv_len.data_ptr(), B, N, max_q, cols, pages, page_size, Hq, Hkv, D, kv_type,
+                         scale, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wn, raw)
     _check(st, "sa_paged_attn")
     return (out, lse) if with_lse else out
 
@@ -613,33 +669,34 @@ def sa_paged_sparse_attn_decode(q, k_pages, v_pages, block_table, idx, count, sc
                                 with_lse: bool = False, ws=None, stream=None):
     """sa_sparse_attn_decode over a paged cache: q [B, Hq, 128]; idx [B, k]
     positions; count [B].  Returns out [B, Hq, 128][, lse [B, Hq] fp32]."""
-    torch = _torch()
-    dev = q.device
-    _tokens(q, "q", dev)
+    dev, shape, _ = _tokens(q, "q")
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     kv_type, Hkv = _pools(k_pages, v_pages, dev)
-    B, Hq, D = q.shape
-    if idx.dim() != 2 or block_table.dim() != 2:
-        raise ValueError("idx must have shape [B, k] and block_table [B, max_pages]")
-    k = idx.shape[1]
-    _ints32(block_table, "block_table", dev, (B, block_table.shape[1]))
-    _ints32(idx, "idx", dev, (B, k))
-    _ints32(count, "count", dev, (B,))
+    B, cols = _table(block_table, dev)
+    if shape[0] != B:
+        raise ValueError(f"q must have shape [{B}, heads, {_D}]: one token per sequence")
+    k = _selection(idx, count, B, dev)
     raw, ctx = _call_stream(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return _sparse(q, k_pages, v_pages, block_table, idx, count, scale, out, with_lse, ws, dev, shape, kv_type,
+                           Hkv, cols, k, raw)
+    return _sparse(q, k_pages, v_pages, block_table, idx, count, scale, out, with_lse, ws, dev, shape, kv_type, Hkv,
+                   cols, k, raw)
+
+
+def _sparse(q, k_pages, v_pages, block_table, idx, count, scale, out, with_lse, ws, dev, shape, kv_type, Hkv, cols, k,
+            raw):
     L = lib()
-    with ctx:
-        if out is None:
-            out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=dev)
-        else:
-            _result(out, "out", dev, (B, Hq, D), torch.bfloat16)
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if with_lse else None
-        wp, wn = _paged_ws_args(L.sa_paged_sparse_attn_decode_workspace(B, Hq, Hkv, D, k, kv_type), ws, dev, raw)
-        st = L.sa_paged_sparse_attn_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                           block_table.data_ptr(), idx.data_ptr(), count.data_ptr(), B,
-                                           block_table.shape[1], k_pages.shape[0], k_pages.shape[1], Hq, Hkv, D, k,
-                                           kv_type, scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                           wp, wn, raw)
+    B, Hq, D = shape
+    out, lse = _outputs(q, shape, out, with_lse, dev)
+    pages, page_size, _ = k_pages.shape
+    wp, wn = _paged_ws_args(L, "sa_paged_sparse_attn_decode_workspace", (B, Hq, Hkv, D, k, kv_type), ws, dev, raw)
+    st = L.sa_paged_sparse_attn_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                                       idx.data_ptr(), count.data_ptr(), B, cols, pages, page_size, Hq, Hkv, D, k,
+                                       kv_type, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wn,
+                                       raw)
     _check(st, "sa_paged_sparse_attn_decode")
     return (out, lse) if with_lse else out
 

@@ -196,7 +196,7 @@ def test_the_binding_refuses_what_it_cannot_pass_on():
     k, v = S.sa_paged_kv_alloc(2, 16, 3, S.SA_KV_E4M3)
     assert k.shape == (2, 16, 400) and k.dtype == torch.uint8 and not v.any()
     assert S.sa_paged_kv_alloc(2, 16, 3)[0].shape == (2, 16, 392)
-    dev = torch.device("cpu")
+    dev = -1   # the CPU's ordinal
     assert S._pools(k, v, dev) == (S.SA_KV_E4M3, 3)
     with pytest.raises(ValueError, match="one shape"):
         S._pools(k, v[:1], dev)
@@ -207,7 +207,7 @@ def test_the_binding_refuses_what_it_cannot_pass_on():
     with pytest.raises(ValueError, match="contiguous"):
         S._pools(k[:, ::2], v[:, ::2], dev)
     with pytest.raises(ValueError, match="CUDA"):
-        S._tokens(torch.zeros(2, 3, 128, dtype=torch.bfloat16), "q", dev)
+        S._tokens(torch.zeros(2, 3, 128, dtype=torch.bfloat16), "q")
     with pytest.raises(ValueError, match="int32"):
         S._ints32(torch.zeros(2, dtype=torch.int64), "kv_len", dev, (2,))
     with pytest.raises(ValueError, match="shape"):
