@@ -353,14 +353,15 @@ constexpr float kRwLift = 9.f, kRwLazy = 6.f;
 // sum, output.  tK, tV: the slice's first row, this kv head; rb: bytes from
 // row to row; sK, sV: the scale bytes of this head in the slice's first row.
 // Key rbase + i is seen by row r when it is <= lim[r] (-1: never).
+// HALF: rows 8 to 15 do not exist (their weights are 0).
 // EDGE: some key of the slice is not seen by some row.  Then V rows that no
 // row sees are zeroed, and infinities and NaN in V are taken out of the
 // product and added to the rows that see them only.
-template <bool FP8, bool EDGE>
+template <bool FP8, bool EDGE, bool HALF>
 __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4], const float (&rowc)[2],
                                          const uint8_t* tK, const uint8_t* tV, int rb, const uint8_t* sK,
                                          const uint8_t* sV, int rbase, const int (&lim)[2], int top) {
-  constexpr int KS = kRwKeys<FP8>, NT = KS / 8;
+  constexpr int KS = kRwKeys<FP8>, NT = KS / 8, NH = HALF ? 1 : 2, NE = 2 * NH;
   const int lane = threadIdx.x & 31, tg = lane & 3, mtx = lane >> 3;
   float sc[NT][4];
 #pragma unroll
@@ -419,7 +420,7 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < NE; ++e) {
       const int hh = e >> 1;
       float z = sc[nt][e] * rowc[hh];
       if constexpr (FP8) z *= kscale[nt][e & 1];
@@ -429,9 +430,9 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
       // (an exponent that is NaN makes the weight NaN, not the reference)
       if constexpr (FP8) mv[hh] = fmaxf(mv[hh], z + vexp[nt][e & 1]);
     }
-  float alpha[2], muse[2];
+  float alpha[2] = {1.f, 1.f}, muse[2];
 #pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
+  for (int hh = 0; hh < NH; ++hh) {
     float v = mx[hh];
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
@@ -441,16 +442,16 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
     st.m[hh] = mnew;
   }
   float rsum[2] = {0.f, 0.f};
-  float wt[NT][4];   // the weights that multiply V
+  float wt[NT][4] = {};   // the weights that multiply V
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < NE; ++e) {
       wt[nt][e] = ex2(sc[nt][e] - muse[e >> 1]);
       rsum[e >> 1] += wt[nt][e];
     }
 #pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
+  for (int hh = 0; hh < NH; ++hh) {
     float v = rsum[hh];
     v += __shfl_xor_sync(0xffffffffu, v, 1);
     v += __shfl_xor_sync(0xffffffffu, v, 2);
@@ -458,7 +459,7 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
   }
   if constexpr (FP8) {   // the output's own reference and weights
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
+    for (int hh = 0; hh < NH; ++hh) {
       float v = mv[hh];
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
@@ -471,7 +472,7 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < NE; ++e) {
         float zo = sc[nt][e] + vexp[nt][e & 1];
         if (EDGE) zo = sc[nt][e] == -INFINITY ? -INFINITY : zo;   // (a masked row's scale may be NaN)
         wt[nt][e] = ex2(zo - mv[e >> 1]);
@@ -482,8 +483,10 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
     for (int dt = 0; dt < 16; ++dt) {
       st.o[dt][0] *= alpha[0];
       st.o[dt][1] *= alpha[0];
-      st.o[dt][2] *= alpha[1];
-      st.o[dt][3] *= alpha[1];
+      if (!HALF) {
+        st.o[dt][2] *= alpha[1];
+        st.o[dt][3] *= alpha[1];
+      }
     }
   }
   bool bad = false;
@@ -542,7 +545,7 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
 #pragma unroll
       for (int dt = 0; dt < 16; ++dt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < NE; ++e) {
           // column of st.o[dt][e]: see the partials' stores
           const int d = FP8 ? (dt >> 1) * 16 + 4 * tg + 2 * (e & 1) + (dt & 1) : dt * 8 + 2 * tg + (e & 1);
           float x;
@@ -554,7 +557,7 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
   }
 }
 
-template <bool FP8, bool SPARSE>
+template <bool FP8, bool SPARSE, bool HALF>
 __global__ void __launch_bounds__(kRwThreads, 1)
 paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__ part_o, float* __restrict__ part_ml,
                        int* __restrict__ err) {
@@ -763,9 +766,9 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
         const uint8_t* tV = tK + (size_t)R * rb;
         const int tail = a.Hkv * kPgD + hs, off = hs * (FP8 ? kPgD : 2 * kPgD);
         if (rbase + kRwKeys<FP8> - 1 > low)
-          row_step<FP8, true>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
+          row_step<FP8, true, HALF>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
         else
-          row_step<FP8, false>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
+          row_step<FP8, false, HALF>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&empty[s]);
@@ -964,7 +967,7 @@ cudaError_t launch_rows(const PagedArgs& a, void* ws, cudaStream_t st) {
   float* po = reinterpret_cast<float*>(p + kRwHead);
   float* pml = reinterpret_cast<float*>(p + kRwHead + align256p(slots * kPgD * 4));
   const size_t smem = kRwBarBytes + (size_t)pl.stages * 2 * pl.R * pl.row_bytes;
-  auto kern = paged_attn_rows_kernel<FP8, SPARSE>;
+  auto kern = pl.RB <= 8 ? paged_attn_rows_kernel<FP8, SPARSE, true> : paged_attn_rows_kernel<FP8, SPARSE, false>;
   cudaError_t e = ensure_dynamic_smem((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((unsigned)pl.W), dim3(kRwThreads), smem, st, a, pl, po, pml, err);
@@ -1017,17 +1020,24 @@ cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_
   return fp8 ? launch_rows<true, false>(a, ws, st) : launch_rows<false, false>(a, ws, st);
 }
 
-// One 16-row block per kv head holds the whole chunk: the row kernel reads
-// the cache once and is bound by HBM.  Longer chunks go to the tensor cores.
-static bool use_rows(int G, int max_q) { return max_q * G <= 16; }
+// Chunks of few query rows per kv head go to the row kernel, which reads the
+// cache once per 16 rows; longer ones to the tensor cores, which read it once
+// per 256.  Measured, us (row kernel / tensor cores; all of the batch alike):
+//   E4M3, 8 kv heads x 4:  20 rows, 4 x 16K positions   82 / 182
+//                          64 rows, 4 x 16K             143 / 184
+//                          128 rows, 1 x 4K             43 / 53;  256 rows 61 / 51
+//   bf16, 8 kv heads x 4:  20 rows, 4 x 16K             113 / 127
+//                          32 rows, 4 x 16K             119 / 127;  64 rows 205 / 129
+// (E4M3 rows are converted for the tensor cores first, so they wait longer.)
+static bool use_rows(int fp8, int G, int max_q) { return (long long)max_q * G <= (fp8 ? 128 : 32); }
 
 size_t paged_attn_workspace_bytes(int fp8, int B, int max_q, long long capacity, int Hkv, int G) {
-  return use_rows(G, max_q) ? paged_rows_workspace_bytes(fp8, B, Hkv, G, max_q)
+  return use_rows(fp8, G, max_q) ? paged_rows_workspace_bytes(fp8, B, Hkv, G, max_q)
                             : paged_tc_workspace_bytes(fp8, B, Hkv, G, max_q, capacity);
 }
 
 cudaError_t launch_paged_attn(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {
-  return use_rows(a.G, a.max_q) ? launch_paged_rows(a, fp8, ws, st) : launch_paged_tc(a, fp8, ws, st);
+  return use_rows(fp8, a.G, a.max_q) ? launch_paged_rows(a, fp8, ws, st) : launch_paged_tc(a, fp8, ws, st);
 }
 
 cudaError_t launch_paged_write(const uint16_t* k_new, const uint16_t* v_new, long long k_stride, long long v_stride,
