@@ -15,7 +15,7 @@
 // instructions (mma.sync, 16 rows) holds the G query heads of the chunk's
 // tokens, which share the kv head's rows.
 //
-//   paged_write_kernel       one warp per (token, K or V)
+//   paged_write_kernel       one warp per token (K and V)
 //   paged_gather_kernel      one warp per selected row (K and V)
 //   paged_attn_rows_kernel   units of (16-row block of queries, tile of
 //       positions, all kv heads), flattened over the batch and cut evenly
@@ -29,39 +29,66 @@ namespace {
 
 // ------------------------------------------------------------------- write
 
-// One new row x (Hkv * 128 bf16) -> a cache row.  Half a warp holds one head:
-// lane j of the half 8 values (16 bytes).
-template <bool FP8>
-__device__ __forceinline__ void write_row(const uint16_t* __restrict__ x, uint8_t* __restrict__ row, int Hkv) {
-  const int lane = threadIdx.x & 31, half = lane >> 4, j = lane & 15;
+// A new row (Hkv * 128 bf16) in registers: half a warp holds one head, lane j
+// of the half 8 values (16 bytes).
+struct NewRow {
   uint4 v[4];
+};
+__device__ __forceinline__ void load_row(NewRow& r, const uint16_t* __restrict__ x, int Hkv) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, j = lane & 15;
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const int h = 2 * it + half;
-    v[it] = h < Hkv ? __ldg(reinterpret_cast<const uint4*>(x + h * kPgD) + j) : make_uint4(0u, 0u, 0u, 0u);
+    r.v[it] = h < Hkv ? __ldg(reinterpret_cast<const uint4*>(x + h * kPgD) + j) : make_uint4(0u, 0u, 0u, 0u);
   }
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Largest magnitude (bf16 bits) of half a warp's head: magnitudes compare as
+// integers, two at a time.  FINITE leaves infinities and NaN out.
+template <bool FINITE>
+__device__ __forceinline__ uint32_t head_max(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a = w[i] & 0x7fff7fffu;
+    if (FINITE) {
+      if ((a & 0xffffu) >= 0x7f80u) a &= 0xffff0000u;
+      if ((a >> 16) >= 0x7f80u) a &= 0x0000ffffu;
+    }
+    m = max_u16x2(m, a);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return max(m & 0xffffu, m >> 16);
+}
+
+// The cache row of a new row.
+template <bool FP8>
+__device__ __forceinline__ void write_row(const NewRow& r, uint8_t* __restrict__ row, int Hkv) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, j = lane & 15;
   if constexpr (!FP8) {
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int h = 2 * it + half;
-      if (h < Hkv) reinterpret_cast<uint4*>(row + h * (2 * kPgD))[j] = v[it];
+      if (h < Hkv) reinterpret_cast<uint4*>(row + h * (2 * kPgD))[j] = r.v[it];
     }
     if (lane == 0) *reinterpret_cast<uint4*>(row + Hkv * (2 * kPgD)) = make_uint4(0u, 0u, 0u, 0u);
   } else {
     uint32_t tail[2] = {0u, 0u};   // the scale bytes of heads 0-3 and 4-7
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
-      // largest finite magnitude: bf16 magnitudes compare as integers
-      uint32_t am = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-        am = max(am, lo < 0x7f80u ? lo : 0u);
-        am = max(am, hi < 0x7f80u ? hi : 0u);
-      }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+      if (2 * it >= Hkv) break;
+      const uint32_t w[4] = {r.v[it].x, r.v[it].y, r.v[it].z, r.v[it].w};
+      uint32_t am = head_max<false>(r.v[it]);
+      const bool odd = __any_sync(0xffffffffu, am >= 0x7f80u);   // rare: not all finite
+      if (odd) am = head_max<true>(r.v[it]);
       // am = 2^(E - 127) * (1 + M / 128); 448 = 2^8 * 1.75, so the least e
       // with am <= 448 * 2^e is E - 135, or E - 134 when 1 + M / 128 > 1.75
       const int E = (int)(am >> 7), M = (int)(am & 0x7fu);
@@ -71,25 +98,30 @@ __device__ __forceinline__ void write_row(const uint16_t* __restrict__ x, uint8_
       uint32_t c[2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float lo = bf_lo(w[i]), hi = bf_hi(w[i]);
-        lo = isinf(lo) ? __uint_as_float(0x7fc00000u) : lo * inv;   // E4M3 has no infinity
-        hi = isinf(hi) ? __uint_as_float(0x7fc00000u) : hi * inv;
-        uint16_t r;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-        if (i & 1) c[i >> 1] |= (uint32_t)r << 16;
-        else c[i >> 1] = r;
+        float lo = bf_lo(w[i]) * inv, hi = bf_hi(w[i]) * inv;
+        if (odd) {   // E4M3 has no infinity
+          lo = isinf(bf_lo(w[i])) ? __uint_as_float(0x7fc00000u) : lo;
+          hi = isinf(bf_hi(w[i])) ? __uint_as_float(0x7fc00000u) : hi;
+        }
+        uint16_t q;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(hi), "f"(lo));
+        if (i & 1) c[i >> 1] |= (uint32_t)q << 16;
+        else c[i >> 1] = q;
       }
       const int h = 2 * it + half;
       if (h < Hkv) reinterpret_cast<uint2*>(row + h * kPgD)[j] = make_uint2(c[0], c[1]);
       const uint32_t b0 = (uint32_t)__shfl_sync(0xffffffffu, e, 0) + 127u;
       const uint32_t b1 = (uint32_t)__shfl_sync(0xffffffffu, e, 16) + 127u;
-      if (2 * it < Hkv) tail[it >> 1] |= b0 << (16 * (it & 1));
+      tail[it >> 1] |= b0 << (16 * (it & 1));
       if (2 * it + 1 < Hkv) tail[it >> 1] |= b1 << (16 * (it & 1) + 8);
     }
     if (lane == 0) *reinterpret_cast<uint4*>(row + Hkv * kPgD) = make_uint4(tail[0], tail[1], 0u, 0u);
   }
 }
 
+// Bound by HBM: 512 bytes in and 258 (E4M3) or 512 out per token, kv head and
+// cache.  A warp takes a token's K and V; its rows are on their way while the
+// token's sequence, position and page are looked up (four dependent reads).
 template <bool FP8>
 __global__ void __launch_bounds__(256)
 paged_write_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new, long long k_stride,
@@ -98,9 +130,11 @@ paged_write_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restric
                    int Hkv, uint8_t* __restrict__ kp, uint8_t* __restrict__ vp, int* dbg) {
   pdl_wait();
   pdl_launch_dependents();
-  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int i = w >> 1;   // token; even warps K, odd warps V
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);   // token
   if (i >= N) return;
+  NewRow k, v;
+  load_row(k, k_new + (long long)i * k_stride, Hkv);
+  load_row(v, v_new + (long long)i * v_stride, Hkv);
   const int b = seq_of_token(q_start, B, i);
   if (b < 0) return;      // in front of the first sequence or behind the last
   const int capacity = max_pages << page_shift;
@@ -114,42 +148,15 @@ paged_write_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restric
   }
   const long long slot = ((long long)pg << page_shift) + (pos & ((1 << page_shift) - 1));
   const long long off = slot * paged_row_bytes(FP8, Hkv);
-  if (w & 1) write_row<FP8>(v_new + (long long)i * v_stride, vp + off, Hkv);
-  else write_row<FP8>(k_new + (long long)i * k_stride, kp + off, Hkv);
+  write_row<FP8>(k, kp + off, Hkv);
+  write_row<FP8>(v, vp + off, Hkv);
 }
 
 // ------------------------------------------------------------------ gather
 
-// One cache row -> a compact bf16 row (Hkv * 128 values, 8 zeros).
-template <bool FP8>
-__device__ __forceinline__ void read_row(const uint8_t* __restrict__ row, uint16_t* __restrict__ dst, int Hkv) {
-  const int lane = threadIdx.x & 31;
-  if constexpr (!FP8) {
-    for (int c = lane; c < Hkv * 16; c += 32)
-      reinterpret_cast<uint4*>(dst)[c] = __ldg(reinterpret_cast<const uint4*>(row) + c);
-  } else {
-    const uint2 tail = __ldg(reinterpret_cast<const uint2*>(row + Hkv * kPgD));
-#pragma unroll
-    for (int it = 0; it < 2; ++it) {   // 8 lanes per head, 16 codes per lane
-      const int h = 4 * it + (lane >> 3), j = lane & 7;
-      if (h >= Hkv) break;
-      const uint4 c = __ldg(reinterpret_cast<const uint4*>(row + h * kPgD) + j);
-      const float s = e8m0_value(((it ? tail.y : tail.x) >> (8 * (h & 3))) & 0xffu);
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      uint32_t r[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e4m3x4_to_f16x4(w[i], r[2 * i], r[2 * i + 1]);
-        r[2 * i] = f16x2_to_bf16x2(r[2 * i], s);
-        r[2 * i + 1] = f16x2_to_bf16x2(r[2 * i + 1], s);
-      }
-      uint4* d = reinterpret_cast<uint4*>(dst + h * kPgD + j * 16);
-      d[0] = make_uint4(r[0], r[1], r[2], r[3]);
-      d[1] = make_uint4(r[4], r[5], r[6], r[7]);
-    }
-  }
-}
-
+// Bound by HBM: a row's bytes in, Hkv * 256 + 16 out, K and V.  One warp per
+// selected row, both caches' loads issued together; 16 lanes take a head, 8
+// values each, so that stores are 512 bytes side by side.
 template <bool FP8>
 __global__ void __launch_bounds__(256)
 paged_gather_kernel(const uint8_t* __restrict__ kp, const uint8_t* __restrict__ vp, const int32_t* __restrict__ table,
@@ -157,27 +164,21 @@ paged_gather_kernel(const uint8_t* __restrict__ kp, const uint8_t* __restrict__ 
                     int page_shift, int Hkv, int k, uint16_t* __restrict__ ko, uint16_t* __restrict__ vo, int* dbg) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, half = lane >> 4, j16 = lane & 15;
   const int b = blockIdx.y;
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (r >= k) return;
   const int c = count[b];
-  uint16_t* dk = ko + ((long long)b * k + r) * (Hkv * kPgD + 8);
-  uint16_t* dv = vo + ((long long)b * k + r) * (Hkv * kPgD + 8);
+  int j = idx[(long long)b * k + r];   // (not used from the count on)
+  uint4* dst[2] = {reinterpret_cast<uint4*>(ko + ((long long)b * k + r) * (Hkv * kPgD + 8)),
+                   reinterpret_cast<uint4*>(vo + ((long long)b * k + r) * (Hkv * kPgD + 8))};
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  if (lane == 0) {
-    reinterpret_cast<uint4*>(dk)[Hkv * 16] = zero;
-    reinterpret_cast<uint4*>(dv)[Hkv * 16] = zero;
-  }
+  if (lane < 2) dst[lane][Hkv * 16] = zero;
   if (r >= c) {
-    for (int e = lane; e < Hkv * 16; e += 32) {
-      reinterpret_cast<uint4*>(dk)[e] = zero;
-      reinterpret_cast<uint4*>(dv)[e] = zero;
-    }
+    for (int e = lane; e < Hkv * 16; e += 32) dst[0][e] = dst[1][e] = zero;
     return;
   }
   const int capacity = max_pages << page_shift;
-  int j = idx[(long long)b * k + r];
   if (j < 0 || j >= capacity) {
     paged_note(dbg, kDbgPagedIndex, j, capacity);
     j = j < 0 ? 0 : capacity - 1;
@@ -185,8 +186,38 @@ paged_gather_kernel(const uint8_t* __restrict__ kp, const uint8_t* __restrict__ 
   const int pg = checked_page(table[(long long)b * max_pages + (j >> page_shift)], num_pages, dbg);
   const long long off =
       (((long long)pg << page_shift) + (j & ((1 << page_shift) - 1))) * paged_row_bytes(FP8, Hkv);
-  read_row<FP8>(kp + off, dk, Hkv);
-  read_row<FP8>(vp + off, dv, Hkv);
+  const uint8_t* row[2] = {kp + off, vp + off};
+  if constexpr (!FP8) {
+    uint4 v[2][4];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+        if (2 * it + half < Hkv) v[kv][it] = __ldg(reinterpret_cast<const uint4*>(row[kv]) + it * 32 + lane);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+        if (2 * it + half < Hkv) dst[kv][it * 32 + lane] = v[kv][it];
+  } else {
+    uint2 v[2][4], tail[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      tail[kv] = __ldg(reinterpret_cast<const uint2*>(row[kv] + Hkv * kPgD));
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+        if (2 * it + half < Hkv) v[kv][it] = __ldg(reinterpret_cast<const uint2*>(row[kv] + (2 * it + half) * kPgD) + j16);
+    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int h = 2 * it + half;
+        if (h < Hkv)
+          dst[kv][h * 16 + j16] =
+              e4m3x8_to_bf16x8(v[kv][it], e8m0_value(((it < 2 ? tail[kv].x : tail[kv].y) >> (8 * (h & 3))) & 0xffu));
+      }
+  }
 }
 
 // ------------------------------------------------------- few-row attention
@@ -1045,7 +1076,7 @@ cudaError_t launch_paged_write(const uint16_t* k_new, const uint16_t* v_new, lon
                                int max_pages, int num_pages, int page_shift, int Hkv, int fp8, uint8_t* kp,
                                uint8_t* vp, int* dbg, cudaStream_t st) {
   if (N <= 0) return cudaSuccess;
-  const dim3 grid((unsigned)((2ll * N + 7) / 8));
+  const dim3 grid((unsigned)((N + 7) / 8));
   const cudaError_t e =
       launch_pdl(fp8 ? paged_write_kernel<true> : paged_write_kernel<false>, grid, dim3(256), 0, st, k_new, v_new,
                  k_stride, v_stride, q_start, kv_len, table, B, N, max_pages, num_pages, page_shift, Hkv, kp, vp, dbg);

@@ -105,6 +105,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// Eight E4M3 codes times `s` -> eight bf16 values.
+__device__ __forceinline__ uint4 e4m3x8_to_bf16x8(uint2 c, float s) {
+  uint32_t r[4];
+  e4m3x4_to_f16x4(c.x, r[0], r[1]);
+  e4m3x4_to_f16x4(c.y, r[2], r[3]);
+  return make_uint4(f16x2_to_bf16x2(r[0], s), f16x2_to_bf16x2(r[1], s), f16x2_to_bf16x2(r[2], s),
+                    f16x2_to_bf16x2(r[3], s));
+}
+
 // The queries of sequence b: packed tokens [begin, begin + len), token t at
 // position pos0 + t of the kv cached positions.  Whatever q_start and kv_len
 // hold, begin and begin + len stay within [0, N] and kv within the table.

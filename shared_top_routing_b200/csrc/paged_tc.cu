@@ -896,22 +896,12 @@ paged_window_kernel(const PagedArgs a, const TcPlan pl, uint16_t* __restrict__ k
         const uint8_t* row = (kv ? a.vp : a.kp) + off;
         uint16_t* dst = (kv ? vw : kw) + to;
 #pragma unroll
-        for (int it = 0; it < 2; ++it) {   // 8 lanes per head, 16 codes per lane
-          const int h = 4 * it + (lane >> 3), j = lane & 7;
+        for (int it = 0; it < 4; ++it) {   // 16 lanes per head, 8 codes per lane
+          const int h = 2 * it + (lane >> 4), j = lane & 15;
           if (h >= pl.nh) break;
-          const uint4 c = __ldg(reinterpret_cast<const uint4*>(row + (pl.h0 + h) * kPgD) + j);
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(row + (pl.h0 + h) * kPgD) + j);
           const float sc = e8m0_value(row[a.Hkv * kPgD + pl.h0 + h]);
-          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-          uint32_t r[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e4m3x4_to_f16x4(w[i], r[2 * i], r[2 * i + 1]);
-            r[2 * i] = f16x2_to_bf16x2(r[2 * i], sc);
-            r[2 * i + 1] = f16x2_to_bf16x2(r[2 * i + 1], sc);
-          }
-          uint4* d = reinterpret_cast<uint4*>(dst + h * kPgD + j * 16);
-          d[0] = make_uint4(r[0], r[1], r[2], r[3]);
-          d[1] = make_uint4(r[4], r[5], r[6], r[7]);
+          reinterpret_cast<uint4*>(dst + h * kPgD)[j] = e4m3x8_to_bf16x8(c, sc);
         }
       }
     }
