@@ -13,11 +13,15 @@
 // tile (they read the same keys); an item is two such tiles, A and B, of one
 // sequence and kv head, with the key tiles up to its last token.  An item with
 // tokens for one tile only lets A take its even key tiles and B its odd ones,
-// and joins them at the end.  The key tiles of all items form one list, cut
-// evenly over one CTA per SM (an item cut in pieces is joined by
-// paged_tc_merge_kernel), so ragged batches and few long sequences load every
-// SM alike.  A and B alternate: while one's scores go through the softmax, the
-// tensor core works for the other.
+// and joins them at the end.  A and B alternate: while one's scores go through
+// the softmax, the tensor core works for the other.
+//
+// Work: one CTA per SM.  Whole items, sorted by length, are dealt out forth
+// and back when that loads the CTAs about evenly (2048 tokens of a prompt, 32
+// heads over 8: 66 us, 104 us when cut; 8192 more of 65536: 7.1 ms, 8.5 ms,
+// the CTAs at work on a head reading the same keys at about the same time).
+// Otherwise - few or uneven items - the key tiles of all items form one list
+// that is cut evenly; an item cut in pieces is joined by paged_tc_merge_kernel.
 //
 // E4M3 caches are first written out in bf16 (exact) by paged_window_kernel, a
 // window of sequences or heads at a time, contiguous: a row is converted once
@@ -58,6 +62,7 @@ constexpr int kStages = 2;
 constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;   // 2 * 152 + 2 * 104 = 4 * 128 per warpgroup at launch
 constexpr int kBadRing = 8;                     // items whose bad-row masks are kept
 constexpr int kBadTiles = 3;                    // key tiles a token of an item may not see in full
+constexpr int kDealItems = 1024, kDealSlack = 4;   // whole items: per kv head at most; key tiles over the even share
 constexpr int kStageRow = 80;                   // bytes of a staged output row: 64 and a pad
 
 // Sequences [b0, b0 + nb) and kv heads [h0, h0 + nh) of a call; for E4M3 their
@@ -71,6 +76,12 @@ struct TcPlan {
   const uint16_t* vw;
 };
 
+// Where a CTA is in the list: sequence b0 + b.
+struct TcIter {
+  int b, qb, kvh, j0;   // j0 < 0: whole items dealt in turn, this one's round ~j0
+  long long left;
+};
+
 struct TcBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_clean[kStages];
@@ -78,15 +89,19 @@ struct TcBars {
   uint64_t drain;
   alignas(16) uint32_t bad[kBadRing][kBadTiles][4];   // V rows with infinities or NaN, by key (read 16 bytes a time)
   long long scan[kTcThreads / 32];
+  int peak[kTcThreads / 32];
+  uint16_t order[kDealItems];   // dealt items from the longest
+  TcIter iter[kTcThreads / 32];   // each warp's place: kept here, not in registers over an item's tiles
   int plan[4];
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(TcBars) <= 1024 && offsetof(TcBars, bad) % 16 == 0 && offsetof(TcBars, scan) % 8 == 0,
+constexpr int kBarBytes = 4096;
+static_assert(sizeof(TcBars) <= kBarBytes && offsetof(TcBars, bad) % 16 == 0 && offsetof(TcBars, scan) % 8 == 0,
               "barrier block");
 
-constexpr size_t kTcSmem = 1024 + 2 * kTileBytes + 2 * kStages * kTileBytes + 1024 + 8 * 32 * kStageRow;
-static_assert(kTcSmem <= 227 * 1024, "shared memory");
+constexpr size_t kTcSmem = 1024 + 2 * kTileBytes + 2 * kStages * kTileBytes + kBarBytes + 8 * 32 * kStageRow;
+static_assert(kTcSmem <= 227 * 1024 && 2 * kDealItems * 4 <= 8 * 32 * kStageRow, "shared memory");
 
 // What a CTA's first piece is, for the merge.
 struct TcPiece {
@@ -117,50 +132,66 @@ __device__ __forceinline__ int item_span(const PagedArgs& a, const TcPlan& pl, i
   return max(1, (max(s.pos0 + t0 + nt, 0) + kTile - 1) / kTile);
 }
 
-// Where a CTA is in the list: sequence b0 + b.
-struct TcIter {
-  int b, qb, kvh, j0;
-  long long left;
-};
+// Dealt items: CTA c's r-th, items from the longest to the shortest, kv heads
+// innermost, every other round backwards.  -1: there is none.
+__device__ __forceinline__ int dealt(const TcPlan& pl, int cta, int r) {
+  const int i = r * pl.W + (r & 1 ? pl.W - 1 - cta : cta);
+  return i < pl.P * pl.nh ? i : -1;
+}
 
-__device__ __forceinline__ bool next_item(const PagedArgs& a, const TcPlan& pl, TcIter& c, TcItem& it) {
-  while (c.left > 0 && c.kvh < pl.nh) {
-    SeqSpan s;
-    int nt;
-    const int n = item_span(a, pl, pl.b0 + c.b, c.qb, s, nt);
-    if (n == 0) {
+// ALL: called by a whole warp (the place is the warp's).
+template <bool ALL>
+__device__ __forceinline__ bool next_item(const PagedArgs& a, const TcPlan& pl, const uint16_t* order, TcIter& place,
+                                          TcItem& it) {
+  TcIter c = place;
+  if (ALL) __syncwarp();
+  SeqSpan s;
+  int nt, n, b, qb, kvh;
+  const bool deal = c.j0 < 0;
+  do {
+    if (deal) {
+      const int i = dealt(pl, blockIdx.x, ~c.j0--);
+      if (i < 0) return false;
+      const int p = order[i / pl.nh];
+      b = p / pl.nqb, qb = p % pl.nqb, kvh = i % pl.nh;
+    } else {
+      if (c.left <= 0 || c.kvh >= pl.nh) return false;
+      b = c.b, qb = c.qb, kvh = c.kvh;
+    }
+    n = item_span(a, pl, pl.b0 + b, qb, s, nt);
+    if (deal && n == 0) return false;   // (the empty ones are the last)
+    if (!deal && (n == 0 || ++c.qb == pl.nqb)) {   // this sequence's last
       c.qb = 0;
       if (++c.b == pl.nb) c.b = 0, ++c.kvh;
-      continue;
     }
-    it.b = pl.b0 + c.b, it.qb = c.qb, it.kvh = c.kvh;
-    it.tok0 = s.begin + c.qb * pl.tpi;
-    it.pos0 = s.pos0 + c.qb * pl.tpi;
-    it.ntA = min(nt, pl.tpt);
-    it.ntB = nt - it.ntA;
-    it.top = max(it.pos0 + nt, 0);
-    it.n = n;
+  } while (n == 0);
+  it.j0 = 0, it.j1 = n;
+  if (!deal) {
     it.j0 = c.j0;
     it.j1 = (int)min((long long)n, c.j0 + c.left);
-    it.split = it.ntB == 0;
-    const int len = it.j1 - it.j0;
-    if (it.split) {
-      it.cntA = (len + 1) / 2;
-      it.cntB = len / 2;
-    } else {
-      const int nA = max(1, (max(it.pos0 + it.ntA, 0) + kTile - 1) / kTile);
-      it.cntA = max(0, min(it.j1, nA) - it.j0);
-      it.cntB = len;
-    }
-    c.left -= len;
+    c.left -= it.j1 - it.j0;
     c.j0 = 0;
-    if (++c.qb == pl.nqb) {
-      c.qb = 0;
-      if (++c.b == pl.nb) c.b = 0, ++c.kvh;
-    }
-    return true;
   }
-  return false;
+  if (!ALL || (threadIdx.x & 31) == 0) place = c;
+  if (ALL) __syncwarp();
+  it.b = pl.b0 + b, it.qb = qb, it.kvh = kvh;
+  it.tok0 = s.begin + qb * pl.tpi;
+  it.pos0 = s.pos0 + qb * pl.tpi;
+  it.ntA = min(nt, pl.tpt);
+  it.ntB = nt - it.ntA;
+  it.top = max(it.pos0 + nt, 0);
+  it.n = n;
+  it.split = it.ntB == 0;
+  const int len = it.j1 - it.j0;
+  if (it.split) {
+    it.cntA = (len + 1) / 2;
+    it.cntB = len / 2;
+  } else {
+    const int nA = max(1, (max(it.pos0 + it.ntA, 0) + kTile - 1) / kTile);
+    it.cntA = max(0, min(it.j1, nA) - it.j0);
+    it.cntB = len;
+  }
+  return true;
 }
 
 // ---- instruction wrappers -------------------------------------------------
@@ -338,7 +369,7 @@ __device__ __forceinline__ void store_rows(unsigned char* stage, const uint32_t*
 }
 
 template <bool LINEAR>
-__device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, const TcPlan& pl, TcIter c, TcBars& bars,
+__device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, const TcPlan& pl, TcIter& c, TcBars& bars,
                                              volatile int* abort_flag, int* err, float* part_o, float* part_ml,
                                              float* scratch, unsigned char* stage, uint32_t tmem) {
   const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
@@ -349,7 +380,7 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
   const bool fits = row < pl.tpt * a.G;
   uint32_t ns = 0, no = 0, items = 0;   // key tiles and pieces so far
   TcItem it;
-  for (; next_item(a, pl, c, it); ++items) {
+  for (; next_item<true>(a, pl, bars.order, c, it); ++items) {
     const int cnt = x ? it.cntB : it.cntA;
     const int nt = x && !it.split ? it.ntB : it.ntA;
     const int t = (x && !it.split ? pl.tpt : 0) + tr;   // token within the item
@@ -531,7 +562,7 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)kDe
 // clocks each on this path, during which the tensor core runs dry, so each
 // tile is waited for once (by the first of A and B that uses it) and before
 // the wait for P, and a product pair O += P V, S = Q K'^T is issued in one go.
-__device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, TcIter c, TcBars& bars,
+__device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, TcIter& c, TcBars& bars,
                                          volatile int* abort_flag, int* err, uint32_t sQ, uint32_t sK, uint32_t sV,
                                          const uint32_t tmem) {
   constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kTile);
@@ -561,7 +592,7 @@ __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, T
     umma_commit(&bars.s_full[x]);
     if (x || it.split) umma_commit(&bars.k_empty[s]);
   };
-  while (ok && next_item(a, pl, c, it)) {
+  while (ok && next_item<false>(a, pl, bars.order, c, it)) {
     const int cnt[2] = {it.cntA, it.cntB};
     const int most = max(cnt[0], cnt[1]);
     const uint32_t mul = it.split ? 2u : 1u;   // tile i of A is mul * i, of B one on when split
@@ -623,7 +654,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   unsigned char* sK = sQ + 2 * kTileBytes;
   unsigned char* sV = sK + kStages * kTileBytes;
   TcBars& bars = *reinterpret_cast<TcBars*>(sV + kStages * kTileBytes);
-  unsigned char* stage = sV + kStages * kTileBytes + 1024;    // output rows, a part per softmax warp
+  unsigned char* stage = sV + kStages * kTileBytes + kBarBytes;   // output rows, a part per softmax warp
   volatile int* abort_flag = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -658,8 +689,15 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   int nt;
   const int per = (pl.P + kTcThreads - 1) / kTcThreads;
   const int p0 = min((int)threadIdx.x * per, pl.P), p1 = min(p0 + per, pl.P);
-  int mine = 0;
-  for (int p = p0; p < p1; ++p) mine += item_span(a, pl, pl.b0 + p / pl.nqb, p % pl.nqb, sp, nt);
+  int mine = 0, longest = 0;
+  int* spans = reinterpret_cast<int*>(stage);   // (in use from here to the roles)
+  for (int p = p0; p < p1; ++p) {
+    const int n = item_span(a, pl, pl.b0 + p / pl.nqb, p % pl.nqb, sp, nt);
+    mine += n;
+    longest = max(longest, n);
+    if (pl.P <= kDealItems) spans[p] = n;
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
   long long before = 0, S = 0;
   {
     long long v = mine;
@@ -668,7 +706,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       const long long y = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += y;
     }
-    if (lane == 31) bars.scan[warp] = v;
+    if (lane == 31) bars.scan[warp] = v, bars.peak[warp] = longest;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -676,6 +714,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     for (int w = 0; w < kTcThreads / 32; ++w) {
       if (w < warp) before += bars.scan[w];
       S += bars.scan[w];
+      longest = max(longest, bars.peak[w]);
     }
     before += v - mine;
   }
@@ -683,6 +722,31 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   const bool idle = (long long)blockIdx.x >= Weff;
   const long long lo = idle ? 0 : blockIdx.x * U / Weff, hi = idle ? 0 : (blockIdx.x + 1) * U / Weff;
   const long long r = idle ? 0 : lo % S;
+  // Whole items dealt to the CTAs instead, when the longest share exceeds the
+  // even one by little: partial results written and joined take the time of
+  // about 5 key tiles.
+  auto even = [&](int load) { return (long long)(load - kDealSlack) * pl.W <= U + U / 16; };
+  bool deal = pl.P <= kDealItems && even(longest);
+  if (deal) {
+    int* sorted = spans + kDealItems;
+    for (int p = p0; p < p1; ++p) {
+      const int n = spans[p];
+      int rank = 0;
+#pragma unroll 8
+      for (int o = 0; o < pl.P; ++o) rank += spans[o] > n || (spans[o] == n && o < p);
+      bars.order[rank] = (uint16_t)p;
+      sorted[rank] = n;
+    }
+    __syncthreads();
+    int load = 0;
+    if ((int)threadIdx.x < pl.W)
+      for (int i, k = 0; (i = dealt(pl, threadIdx.x, k)) >= 0; ++k) load += sorted[i / pl.nh];
+    load = __reduce_max_sync(0xffffffffu, load);
+    if (lane == 0) bars.peak[warp] = load;
+    __syncthreads();
+    for (int w = 0; w < kTcThreads / 32; ++w) load = max(load, bars.peak[w]);
+    deal = even(load);
+  }
   if (!idle && before <= r && r < before + mine) {
     long long at = before;
     for (int p = p0; p < p1; ++p) {
@@ -699,17 +763,20 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   if (threadIdx.x == 0 && *err != 0) bars.abort = 1;   // an earlier call failed: every output shows it
   __syncthreads();
   const uint32_t tmem = bars.tmem_base;
-  TcIter c;
-  c.b = idle ? 0 : bars.plan[0];
-  c.qb = idle ? 0 : bars.plan[1];
-  c.kvh = idle ? 0 : (int)(lo / S);
-  c.j0 = idle ? 0 : bars.plan[2];
-  c.left = hi - lo;
+  TcIter c0;
+  c0.b = idle ? 0 : bars.plan[0];
+  c0.qb = idle ? 0 : bars.plan[1];
+  c0.kvh = idle ? 0 : (int)(lo / S);
+  c0.j0 = deal ? -1 : idle ? 0 : bars.plan[2];
+  c0.left = hi - lo;
+  TcIter& c = bars.iter[warp];
+  if (lane == 0) c = c0;
+  __syncwarp();
   if (threadIdx.x == 0) {
     TcPiece pc = {};
-    TcIter c2 = c;
+    TcIter c2 = c0;
     TcItem it;
-    if (next_item(a, pl, c2, it)) pc = {it.b, it.qb, it.kvh, it.j0, it.j1, it.n, 1, 0};
+    if (!deal && next_item<false>(a, pl, bars.order, c2, it)) pc = {it.b, it.qb, it.kvh, it.j0, it.j1, it.n, 1, 0};
     pieces[blockIdx.x] = pc;
   }
   float* my_scratch = scratch + (size_t)blockIdx.x * kTile * (kPgD + 2);
@@ -728,7 +795,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       const uint32_t piece_bytes = (uint32_t)piece * 128u;   // of one half
       TcItem it;
       bool ok = true;
-      while (ok && next_item(a, pl, c, it)) {
+      while (ok && next_item<true>(a, pl, bars.order, c, it)) {
         const int32_t* trow = a.table + (long long)it.b * a.max_pages;
         const int e_last = !LINEAR && it.top > 0 ? (it.top - 1) >> a.page_shift : 0;
         int e0 = it.j0 * kTile >> a.page_shift;
@@ -795,7 +862,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const uint32_t bytes = (uint32_t)(pl.tpt * a.G) * 256u;
         TcItem it;
         bool ok = true;
-        while (ok && next_item(a, pl, c, it)) {
+        while (ok && next_item<false>(a, pl, bars.order, c, it)) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (!ok || (x ? it.cntB : it.cntA) == 0) continue;   // (a split item's rows go to both)
@@ -827,7 +894,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     uint32_t seq = 0, items = 0;
     TcItem it;
     bool ok = true;
-    for (; next_item(a, pl, c, it); ++items) {   // (after an abort too: the barrier below takes all four warps)
+    for (; next_item<true>(a, pl, bars.order, c, it); ++items) {   // (after an abort too: the barrier below takes all four warps)
       uint32_t(*bad)[4] = bars.bad[items % kBadRing];
       if (t < kBadTiles * 4) bad[t >> 2][t & 3] = 0u;
       named_sync(3, 128);
