@@ -223,9 +223,13 @@ paged_gather_kernel(const uint8_t* __restrict__ kp, const uint8_t* __restrict__ 
 // ------------------------------------------------------- few-row attention
 
 constexpr int kRwConsumers = 8;
-constexpr int kRwThreads = (kRwConsumers + 1) * 32;
+// The producer has three idle warps beside it, whose registers the consumers
+// take (8 * 224 + 4 * 56 = 12 * 168; without: 121 us for one token of each of
+// 8 x 32K E4M3 positions, 115 with).
+constexpr int kRwThreads = (kRwConsumers + 4) * 32, kRwConsumerRegs = 224, kRwOtherRegs = 56;
 constexpr int kRwMaxStages = 8;
-constexpr int kRwBarBytes = 256;       // mbarriers, abort word, plan
+constexpr int kRwBarBytes = 256;       // mbarriers, abort word, plan, scan
+static_assert((2 * kRwMaxStages + 2 + kRwThreads / 32) * 8 <= kRwBarBytes, "barrier block");
 constexpr int kRwStageBytes = 222 * 1024;
 constexpr int kRwMergeThreads = 256;
 constexpr int kRwMergeMaxC = 1280;     // contributors of one (row block, head)
@@ -597,7 +601,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
   uint64_t* empty = full + kRwMaxStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + kRwMaxStages);
   int* sh_plan = const_cast<int*>(abort_flag) + 1;                            // first item and its first tile
-  long long* sh_scan = reinterpret_cast<long long*>(empty + kRwMaxStages + 2);   // 9 words
+  long long* sh_scan = reinterpret_cast<long long*>(empty + kRwMaxStages + 2);   // a word per warp
   unsigned char* ring = smem + kRwBarBytes;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rb = pl.row_bytes, R = pl.R;
@@ -640,8 +644,10 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
   int p = sh_plan[0], tile = sh_plan[1];
   long long left = hi - lo;
 
-  if (warp == kRwConsumers) {
+  if (warp >= kRwConsumers) {
     // ------------------------------------------------------------ producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRwOtherRegs));
+    if (warp > kRwConsumers) return;   // (registers are split by four warps)
     uint32_t fill = 0;
     const int page_mask = (1 << a.page_shift) - 1;
     bool ok = true;
@@ -756,6 +762,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
   }
 
   // -------------------------------------------------------------- consumers
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRwConsumerRegs));
   const int gq = lane >> 2, tg = lane & 3;
   const int hs = warp / pl.wph, rs = warp % pl.wph;
   const bool active = hs < a.Hkv;
@@ -836,8 +843,6 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
 
 // One CTA per (token, query head): out = sum_x w_x o_x / L, w_x = 2^(m_x - M),
 // L = sum_x w_x l_x, M = max_x m_x over the contributors x of its row block.
-// (64 registers a thread, so that it is resident beside the kernel before and
-// has its place in the list worked out when that ends.)
 template <bool SPARSE>
 __global__ void __launch_bounds__(kRwMergeThreads, 4)
 paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* __restrict__ part_o,
