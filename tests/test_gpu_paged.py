@@ -435,6 +435,86 @@ def test_a_long_chunk_is_the_same_every_time(kv_type):
         assert (err <= 2.0 ** -8 * (mag + o.abs()) * 1.01 + 2.0 ** -10 * mag).all()
 
 
+@pytest.mark.parametrize("kv_type", TYPES)
+@pytest.mark.parametrize("hkv,G,top", [(1, 1, 32), (2, 4, 8), (1, 8, 16), (3, 16, 8), (8, 5, 6)])
+def test_short_chunks_of_every_length(kv_type, hkv, G, top):
+    """Chunks that take one block of rows up to those that take many."""
+    q_len = [1 + (7 * i) % top for i in range(9)] + [top]
+    _check_attn(*_attn_case(G, kv_type, hkv, G, 16, q_len, [n + 37 * i for i, n in enumerate(q_len)]))
+
+
+@pytest.mark.parametrize("kv_type", TYPES)
+@pytest.mark.parametrize("B,hkv,G", [
+    (5, 2, 4),       # a few items per SM at most
+    (70, 3, 16),     # more items per kv head than threads of a block
+    (130, 1, 16),    # more than are sorted: the list is cut
+])
+def test_ragged_batches_of_many_items(kv_type, B, hkv, G):
+    q_len = [1 + 13 * i % 11 for i in range(B)]
+    q_len[B // 2] = 130
+    kv = [n + (29 * i) % 150 for i, n in enumerate(q_len)]
+    _check_attn(*_attn_case(B, kv_type, hkv, G, 32, q_len, kv))
+
+
+@pytest.mark.parametrize("kv_type", TYPES)
+@pytest.mark.parametrize("lens", [[1000] * 4, [2000, 300, 77, 900]])
+def test_whole_prompts(kv_type, lens):
+    """Items dealt to the CTAs whole, of one length and of many; every run the
+    same bits."""
+    hkv, G, page = 8, 2, 64
+    g = torch.Generator(device=dev()).manual_seed(4)
+    pages = [-(-n // page) for n in lens]
+    pools = sa.sa_paged_kv_alloc(sum(pages), page, hkv, kv_type, device=dev())
+    table, at = np.zeros((len(lens), max(pages)), np.int32), 0
+    for b, n in enumerate(pages):
+        table[b, :n] = np.arange(at, at + n)[::-1]
+        at += n
+    N = sum(lens)
+    start = np.cumsum([0] + lens)
+    k, v = (torch.randn(N, hkv, 128, device=dev(), generator=g).bfloat16() for _ in range(2))
+    args = (i32(table), i32(start), i32(lens))
+    sa.sa_paged_kv_write(k, v, *pools, *args)
+    q = torch.randn(N, hkv * G, 128, device=dev(), generator=g).bfloat16()
+    out, lse = sa.sa_paged_attn(q, *pools, *args, max(lens), with_lse=True)
+    for _ in range(4):
+        o2, l2 = sa.sa_paged_attn(q, *pools, *args, max(lens), with_lse=True)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    for b, n in enumerate(lens):
+        idx = torch.arange(n, device=dev(), dtype=torch.int32)[None]
+        rows = sa.sa_paged_kv_gather(*pools, i32(table[b:b + 1]), idx, i32([n]))
+        kr, vr = (r[0, :, :hkv * 128].double().view(n, hkv, 128).transpose(0, 1) for r in rows)
+        part = slice(start[b], start[b + 1])
+        qb = q[part].double().view(n, hkv, G, 128).permute(1, 2, 0, 3)
+        z = torch.matmul(qb, kr.transpose(1, 2)[:, None]) * 128 ** -0.5
+        seen = torch.ones(n, n, dtype=torch.bool, device=dev()).tril()
+        zabs = (torch.matmul(qb.abs(), kr.abs().transpose(1, 2)[:, None]) * seen).amax(-1) * 128 ** -0.5
+        z.masked_fill_(~seen, float("-inf"))
+        ref = torch.logsumexp(z, -1)
+        p = torch.exp(z - ref[..., None])
+        o, mag = torch.matmul(p, vr[:, None]), torch.matmul(p, vr.abs()[:, None])
+
+        def flat(t):   # [hkv, G, n, ...] as [n, hkv * G, ...]
+            return t.movedim(2, 0).reshape(n, hkv * G, *t.shape[3:]).cpu().numpy()
+
+        _check_attn(out[part], lse[part], tuple(flat(t) for t in (o, ref, mag, zabs)), n)
+
+
+@pytest.mark.parametrize("B,hkv,max_pages", [(3, 8, 5000), (2, 8, 30000), (2, 1, 140000)])
+def test_codes_written_out_in_rounds(B, hkv, max_pages):
+    """A block table so wide that the rows of all sequences, or of all heads of
+    one, do not fit the space for rows in bf16: a few at a time."""
+    G, page, q_len, kv = 16, 16, [40, 9, 150][:B], [333, 140, 170][:B]
+    table, num_pages = _table(kv, page, _rng(B))
+    wide = np.full((B, max_pages), -3, np.int32)
+    wide[:, :table.shape[1]] = table
+    pools = [_random_pool(140 + i, num_pages, page, hkv, P.E4M3) for i in range(2)]
+    q_start = np.cumsum([0] + q_len).astype(np.int32)
+    q = _normal(30, 1, (int(q_start[-1]), hkv * G, 128))
+    out, lse = sa.sa_paged_attn(to_dev(q), *[_dev_pool(p, P.E4M3) for p in pools], i32(wide), i32(q_start), i32(kv),
+                                max(q_len), with_lse=True)
+    _check_attn(out, lse, P.paged_attention(q, *pools, table, q_start, kv, P.E4M3), max(kv))
+
+
 # ---------------------------------------------------------- in use together
 
 @pytest.mark.parametrize("kv_type", TYPES)
