@@ -1059,11 +1059,11 @@ cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_
 // Chunks of few query rows per kv head go to the row kernel, which reads the
 // cache once per 16 rows; longer ones to the tensor cores, which read it once
 // per 256.  Measured, us (row kernel / tensor cores; all of the batch alike):
-//   E4M3, 8 kv heads x 4:  20 rows, 4 x 16K positions   82 / 182
-//                          64 rows, 4 x 16K             143 / 184
-//                          128 rows, 1 x 4K             43 / 53;  256 rows 61 / 51
-//   bf16, 8 kv heads x 4:  20 rows, 4 x 16K             113 / 127
-//                          32 rows, 4 x 16K             119 / 127;  64 rows 205 / 129
+//   E4M3, 8 kv heads x 4:  20 rows, 4 x 16K positions   76 / 209
+//                          64 rows, 4 x 16K             133 / 209
+//                          128 rows, 1 x 4K             37 / 55;  256 rows 55 / 53
+//   bf16, 8 kv heads x 4:  20 rows, 4 x 16K             111 / 127
+//                          32 rows, 4 x 16K             115 / 127;  64 rows 197 / 131
 // (E4M3 rows are converted for the tensor cores first, so they wait longer.)
 static bool use_rows(int fp8, int G, int max_q) { return (long long)max_q * G <= (fp8 ? 128 : 32); }
 
