@@ -232,6 +232,10 @@ constexpr int kRwBarBytes = 256;       // mbarriers, abort word, plan, scan
 static_assert((2 * kRwMaxStages + 2 + kRwThreads / 32) * 8 <= kRwBarBytes, "barrier block");
 constexpr int kRwStageBytes = 222 * 1024;
 constexpr int kRwMergeThreads = 256;
+// Rows from which a warp folds one, not a CTA (us, whole call, E4M3, one token
+// of each sequence, 32 heads, warp / CTA: 64 x 4K positions 121 / 127, 32 x 4K
+// 78 / 80, 16 x 4K 53 / 51, 1M selected from 35 / 18).
+constexpr int kRwMergeMany = 1024;
 constexpr int kRwMergeMaxC = 1280;     // contributors of one (row block, head)
 
 // Positions a consumer warp takes per step: codes are half the bytes, so twice
@@ -841,56 +845,50 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
   }
 }
 
-// One CTA per (token, query head): out = sum_x w_x o_x / L, w_x = 2^(m_x - M),
-// L = sum_x w_x l_x, M = max_x m_x over the contributors x of its row block.
-template <bool SPARSE>
-__global__ void __launch_bounds__(kRwMergeThreads, 4)
+// out = sum_x w_x o_x / L, w_x = 2^(m_x - M), L = sum_x w_x l_x, M = max_x m_x
+// over the contributors x of a row's block.  MANY: one CTA per token and 8
+// query heads, a warp each; otherwise one CTA per row.
+template <bool SPARSE, bool MANY>
+__global__ void __launch_bounds__(kRwMergeThreads, MANY ? 3 : 4)
 paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* __restrict__ part_o,
                              const float* __restrict__ part_ml, const int* __restrict__ err) {
   constexpr int kWarps = kRwMergeThreads / 32;
   constexpr int kPre = 8;
-  __shared__ float wts[kRwMergeMaxC];
-  __shared__ float red[kWarps][kPgD];
-  __shared__ float rmax[kWarps], rsum[kWarps];
-  __shared__ long long sh_scan[kWarps];
+  __shared__ long long sh_scan[kWarps], sh_at;
+  __shared__ int sh_item[3];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tok = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const int hs = h / a.G, gq = h % a.G;
-  int p = tok, row = gq;
-  if constexpr (!SPARSE) {
-    const int b = seq_of_token(a.q_start, a.B, tok);
-    if (b < 0) return;
-    const SeqSpan s = seq_span(a.q_start, a.kv_len, b, a.N, a.max_pages << a.page_shift);
-    const int t = tok - s.begin;
-    if (t >= a.max_q) return;
-    p = b * pl.nrb + t / pl.tb;
-    row = t % pl.tb * a.G + gq;
-  }
-  // tiles before item p and in all
-  long long v = 0, pre_tiles = 0;
-  for (int i = tid; i < pl.P; i += kRwMergeThreads) {
+  const int hb = MANY ? (a.Hq + kWarps - 1) / kWarps : a.Hq;
+  const int tok = blockIdx.x / hb, h = MANY ? blockIdx.x % hb * kWarps + warp : blockIdx.x % hb;
+  // the token's item, the tiles before it and in all
+  if (tid == 0) sh_item[0] = -1;
+  const int per = (pl.P + kRwMergeThreads - 1) / kRwMergeThreads;
+  const int p0 = min(tid * per, pl.P), p1 = min(p0 + per, pl.P);
+  int mine = 0, hit = -1, hit_at = 0, hit_n = 0, hit_row = 0;
+  for (int i = p0; i < p1; ++i) {
     const int n = item_tiles<SPARSE>(a, pl, i);
-    v += n;
-    if (i < p) pre_tiles += n;
+    bool here = i == tok;
+    int t = 0;
+    if constexpr (!SPARSE) {
+      const SeqSpan s = seq_span(a.q_start, a.kv_len, i / pl.nrb, a.N, a.max_pages << a.page_shift);
+      t = tok - s.begin - i % pl.nrb * pl.tb;
+      here = t >= 0 && t < pl.tb && t + i % pl.nrb * pl.tb < min(s.len, a.max_q);
+    }
+    if (here) hit = i, hit_at = mine, hit_n = n, hit_row = t * a.G;
+    mine += n;
   }
-  const int n_p = item_tiles<SPARSE>(a, pl, p);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v += __shfl_xor_sync(0xffffffffu, v, o);
-    pre_tiles += __shfl_xor_sync(0xffffffffu, pre_tiles, o);
-  }
-  __shared__ long long sh_pre[kWarps];
-  if (lane == 0) {
-    sh_scan[warp] = v;
-    sh_pre[warp] = pre_tiles;
+  long long before;
+  const long long U = block_scan<kRwMergeThreads>(mine, before, sh_scan);
+  if (hit >= 0) {
+    sh_item[0] = hit;
+    sh_item[1] = hit_n;
+    sh_item[2] = hit_row;
+    sh_at = before + hit_at;
   }
   __syncthreads();
-  long long U = 0, base_u = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    U += sh_scan[w];
-    base_u += sh_pre[w];
-  }
+  const int p = sh_item[0], n_p = sh_item[1];
+  if (p < 0) return;   // of no sequence, or beyond the bound
+  const int hs = min(h, a.Hq - 1) / a.G, row = sh_item[2] + h % a.G;
+  const long long base_u = sh_at;
   const long long Weff = U < pl.W ? U : pl.W;
   // the CTA that owns unit u: the largest c with floor(c U / W) <= u
   const long long first = n_p ? ((base_u + 1) * Weff - 1) / U : 0;
@@ -900,6 +898,57 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
   const long long e0 = (((long long)p + first) * pl.wph * a.Hkv + hs) * pl.RB + row;
   const float* pml = part_ml + e0 * 2;
   const float* po = part_o + e0 * kPgD;
+  const long long at = (long long)tok * a.Hq + h;
+  if constexpr (MANY) {
+    if (h >= a.Hq) return;
+    pdl_wait();
+    pdl_launch_dependents();
+    const bool failed = *err != 0;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = 0; x0 < C; x0 += 32) {
+      const int nx = min(32, C - x0);
+      const float* ox = po + x0 * xstride * kPgD;
+      float4 pre[kPre];
+#pragma unroll
+      for (int i = 0; i < kPre; ++i)
+        if (i < nx) pre[i] = __ldcg(reinterpret_cast<const float4*>(ox + i * xstride * kPgD) + lane);
+      const float2 ml = lane < nx ? __ldcg(reinterpret_cast<const float2*>(pml + (x0 + lane) * xstride * 2))
+                                  : make_float2(-INFINITY, 0.f);
+      const float m = fmaxf(M, warp_max(ml.x));
+      // (a NaN sum counts: it belongs in the result)
+      const float w = ml.x != -INFINITY || ml.y != 0.f ? exp2f(ml.x - m) : 0.f;
+      const float f = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : exp2f(M - m);
+      M = m;
+      L = (f != 0.f ? L * f : 0.f) + warp_sum(w != 0.f ? ml.y * w : 0.f);
+      acc = f != 0.f ? make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      auto fold = [&](float4 ov, int i) {
+        const float wt = __shfl_sync(0xffffffffu, w, i);
+        if (wt == 0.f) return;
+        acc.x = fmaf(ov.x, wt, acc.x);
+        acc.y = fmaf(ov.y, wt, acc.y);
+        acc.z = fmaf(ov.z, wt, acc.z);
+        acc.w = fmaf(ov.w, wt, acc.w);
+      };
+#pragma unroll
+      for (int i = 0; i < kPre; ++i)
+        if (i < nx) fold(pre[i], i);
+#pragma unroll 4
+      for (int i = kPre; i < nx; ++i)
+        fold(__ldcg(reinterpret_cast<const float4*>(ox + i * xstride * kPgD) + lane), i);
+    }
+    const bool none = L == 0.f;   // nothing to attend to
+    const float inv = failed ? __int_as_float(0x7fc00000) : (none ? 0.f : 1.f / L);
+    reinterpret_cast<uint2*>(a.out + at * kPgD)[lane] =
+        none && !failed ? make_uint2(0u, 0u)
+                        : make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && a.lse != nullptr)
+      a.lse[at] = failed ? __int_as_float(0x7fc00000) : (none ? -INFINITY : (M + log2f(L)) * kPgLn2);
+    return;
+  }
+  __shared__ float wts[kRwMergeMaxC];
+  __shared__ alignas(16) float red[kWarps][kPgD];   // (stored 16 bytes at a time)
+  __shared__ float rmax[kWarps], rsum[kWarps];
   pdl_wait();
   pdl_launch_dependents();
   const float2 ml0 = tid < C ? __ldcg(reinterpret_cast<const float2*>(pml + (long long)tid * xstride * 2))
@@ -965,7 +1014,6 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
     for (int w = 0; w < kWarps; ++w) o += red[w][tid];
     const bool none = L == 0.f;   // nothing to attend to
     const float res = none ? 0.f : o / L;
-    const long long at = (long long)tok * a.Hq + h;
     // a kernel that gave up leaves NaN, so the failure is visible
     a.out[at * kPgD + tid] = failed ? (uint16_t)0x7fc0 : (uint16_t)(pack_bf16x2(res, 0.f) & 0xffffu);
     if (tid == 0 && a.lse != nullptr)
@@ -1008,8 +1056,14 @@ cudaError_t launch_rows(const PagedArgs& a, void* ws, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((unsigned)pl.W), dim3(kRwThreads), smem, st, a, pl, po, pml, err);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_attn_rows_merge_kernel<SPARSE>, dim3((unsigned)((long long)a.N * a.Hq)), dim3(kRwMergeThreads),
-                 0, st, a, pl, po, pml, err);
+  constexpr int kWarps = kRwMergeThreads / 32;
+  if ((long long)a.N * a.Hq >= kRwMergeMany)
+    e = launch_pdl(paged_attn_rows_merge_kernel<SPARSE, true>,
+                   dim3((unsigned)((long long)a.N * ((a.Hq + kWarps - 1) / kWarps))), dim3(kRwMergeThreads), 0, st, a,
+                   pl, po, pml, err);
+  else
+    e = launch_pdl(paged_attn_rows_merge_kernel<SPARSE, false>, dim3((unsigned)((long long)a.N * a.Hq)),
+                   dim3(kRwMergeThreads), 0, st, a, pl, po, pml, err);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
