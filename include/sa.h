@@ -345,7 +345,11 @@ sa_status sa_paged_kv_gather(const void* k_pages, const void* v_pages, const int
  *         tokens that belong to no sequence are left as they were
  *   ws    >= sa_paged_attn_workspace(...) bytes (zero-filled before first
  *         use; see the conventions above).  Its first int32 is the kernel
- *         error word: 0 after a good call, else the outputs hold NaN.
+ *         error word: 0 after a good call, else the outputs hold NaN.  Long
+ *         chunks of an E4M3 cache keep rows in bf16 there, up to 1 GiB at a
+ *         time (or one kv head of one sequence), with room for max_pages pages
+ *         of every sequence: a table no wider than the longest sequence needs
+ *         takes fewer rounds.
  * Supported: Hq % Hkv == 0; Hq/Hkv <= 16; N * Hq < 2^31. */
 size_t sa_paged_attn_workspace(int B, int N, int max_q, int max_pages, int page_size, int Hq, int Hkv, int D,
                                int kv_type);

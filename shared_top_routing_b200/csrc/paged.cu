@@ -250,6 +250,7 @@ struct RowsPlan {
   int wph, R;              // consumer warps per kv head, positions per tile
   int row_bytes, stages;
   int W;                   // CTAs
+  bool by_item;            // merge: CTAs by row block and token, not by token (most tokens are not here)
 };
 
 // Tiles of item p: the positions its last token attends to, or the selected
@@ -262,7 +263,7 @@ __device__ __forceinline__ int item_keys(const PagedArgs& a, const RowsPlan& pl,
     const int b = p / pl.nrb, t0 = p % pl.nrb * pl.tb;
     const SeqSpan s = seq_span(a.q_start, a.kv_len, b, a.N, a.max_pages << a.page_shift);
     const int n = min(s.len, a.max_q);
-    if (t0 >= n) return 0;
+    if (t0 >= n || s.len > a.many) return 0;
     return max(s.pos0 + min(t0 + pl.tb, n), 0);
   }
 }
@@ -858,7 +859,18 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
   __shared__ int sh_item[3];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hb = MANY ? (a.Hq + kWarps - 1) / kWarps : a.Hq;
-  const int tok = blockIdx.x / hb, h = MANY ? blockIdx.x % hb * kWarps + warp : blockIdx.x % hb;
+  const int h = MANY ? blockIdx.x % hb * kWarps + warp : blockIdx.x % hb;
+  int tok = blockIdx.x / hb, p_by = -1, t_by = 0;
+  if (!SPARSE && pl.by_item) {
+    p_by = tok / pl.tb, t_by = tok % pl.tb;
+    const SeqSpan s = seq_span(a.q_start, a.kv_len, p_by / pl.nrb, a.N, a.max_pages << a.page_shift);
+    const int t = p_by % pl.nrb * pl.tb + t_by;
+    if (t >= min(s.len, a.max_q) || s.len > a.many) {
+      pdl_wait();
+      return;
+    }
+    tok = s.begin + t;
+  }
   // the token's item, the tiles before it and in all
   if (tid == 0) sh_item[0] = -1;
   const int per = (pl.P + kRwMergeThreads - 1) / kRwMergeThreads;
@@ -866,9 +878,9 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
   int mine = 0, hit = -1, hit_at = 0, hit_n = 0, hit_row = 0;
   for (int i = p0; i < p1; ++i) {
     const int n = item_tiles<SPARSE>(a, pl, i);
-    bool here = i == tok;
-    int t = 0;
-    if constexpr (!SPARSE) {
+    bool here = i == (SPARSE ? tok : p_by);
+    int t = t_by;
+    if (!SPARSE && !pl.by_item) {
       const SeqSpan s = seq_span(a.q_start, a.kv_len, i / pl.nrb, a.N, a.max_pages << a.page_shift);
       t = tok - s.begin - i % pl.nrb * pl.tb;
       here = t >= 0 && t < pl.tb && t + i % pl.nrb * pl.tb < min(s.len, a.max_q);
@@ -886,7 +898,10 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
   }
   __syncthreads();
   const int p = sh_item[0], n_p = sh_item[1];
-  if (p < 0) return;   // of no sequence, or beyond the bound
+  if (p < 0) {   // of no sequence, or beyond the bound
+    pdl_wait();
+    return;
+  }
   const int hs = min(h, a.Hq - 1) / a.G, row = sh_item[2] + h % a.G;
   const long long base_u = sh_at;
   const long long Weff = U < pl.W ? U : pl.W;
@@ -1030,6 +1045,7 @@ RowsPlan rows_plan(int fp8, int B, int Hkv, int G, int max_q) {
   pl.wph = kRwConsumers / Hkv;   // 8, 4, 2 or 1 for Hkv <= 8: tiles and pages are powers of two, neither
   pl.R = (fp8 ? kRwKeys<true> : kRwKeys<false>) * pl.wph;   // straddles the other
   pl.row_bytes = paged_row_bytes(fp8, Hkv);
+  pl.by_item = false;
   const int stage = 2 * pl.R * pl.row_bytes;
   pl.stages = kRwStageBytes / stage < kRwMaxStages ? kRwStageBytes / stage : kRwMaxStages;
   pl.W = device_sm_count();
@@ -1043,13 +1059,12 @@ constexpr size_t kRwHead = 256;   // the kernel error word
 size_t rows_slots(const RowsPlan& pl, int Hkv) { return (size_t)(pl.P + pl.W) * pl.wph * Hkv * pl.RB; }
 
 template <bool FP8, bool SPARSE>
-cudaError_t launch_rows(const PagedArgs& a, void* ws, cudaStream_t st) {
-  const RowsPlan pl = rows_plan(FP8, a.B, a.Hkv, a.G, SPARSE ? 1 : a.max_q);
+cudaError_t launch_rows(const PagedArgs& a, void* parts, int* err, cudaStream_t st) {
+  RowsPlan pl = rows_plan(FP8, a.B, a.Hkv, a.G, SPARSE ? 1 : a.max_q);
   const size_t slots = rows_slots(pl, a.Hkv);
-  char* p = static_cast<char*>(ws);
-  int* err = reinterpret_cast<int*>(p);
-  float* po = reinterpret_cast<float*>(p + kRwHead);
-  float* pml = reinterpret_cast<float*>(p + kRwHead + align256p(slots * kPgD * 4));
+  char* p = static_cast<char*>(parts);
+  float* po = reinterpret_cast<float*>(p);
+  float* pml = reinterpret_cast<float*>(p + align256p(slots * kPgD * 4));
   const size_t smem = kRwBarBytes + (size_t)pl.stages * 2 * pl.R * pl.row_bytes;
   auto kern = pl.RB <= 8 ? paged_attn_rows_kernel<FP8, SPARSE, true> : paged_attn_rows_kernel<FP8, SPARSE, false>;
   cudaError_t e = ensure_dynamic_smem((const void*)kern, smem);
@@ -1057,12 +1072,15 @@ cudaError_t launch_rows(const PagedArgs& a, void* ws, cudaStream_t st) {
   e = launch_pdl(kern, dim3((unsigned)pl.W), dim3(kRwThreads), smem, st, a, pl, po, pml, err);
   if (e != cudaSuccess) return e;
   constexpr int kWarps = kRwMergeThreads / 32;
-  if ((long long)a.N * a.Hq >= kRwMergeMany)
+  const long long by_item = (long long)pl.P * pl.tb;
+  pl.by_item = !SPARSE && by_item < a.N;
+  const long long tokens = pl.by_item ? by_item : a.N;
+  if (tokens * a.Hq >= kRwMergeMany)
     e = launch_pdl(paged_attn_rows_merge_kernel<SPARSE, true>,
-                   dim3((unsigned)((long long)a.N * ((a.Hq + kWarps - 1) / kWarps))), dim3(kRwMergeThreads), 0, st, a,
-                   pl, po, pml, err);
+                   dim3((unsigned)(tokens * ((a.Hq + kWarps - 1) / kWarps))), dim3(kRwMergeThreads), 0, st, a, pl, po,
+                   pml, err);
   else
-    e = launch_pdl(paged_attn_rows_merge_kernel<SPARSE, false>, dim3((unsigned)((long long)a.N * a.Hq)),
+    e = launch_pdl(paged_attn_rows_merge_kernel<SPARSE, false>, dim3((unsigned)(tokens * a.Hq)),
                    dim3(kRwMergeThreads), 0, st, a, pl, po, pml, err);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -1097,17 +1115,25 @@ cudaError_t paged_dbg_read(int* host4, bool reset) {
 #endif
 }
 
-size_t paged_rows_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q) {
+size_t paged_rows_part_bytes(int fp8, int B, int Hkv, int G, int max_q) {
   const RowsPlan pl = rows_plan(fp8, B, Hkv, G, max_q);
   const size_t slots = rows_slots(pl, Hkv);
-  return kRwHead + align256p(slots * kPgD * 4) + align256p(slots * 2 * 4);
+  return align256p(slots * kPgD * 4) + align256p(slots * 2 * 4);
+}
+
+size_t paged_rows_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q) {
+  return kRwHead + paged_rows_part_bytes(fp8, B, Hkv, G, max_q);
+}
+
+cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* parts, int* err, cudaStream_t st) {
+  if (a.N <= 0) return cudaSuccess;
+  if (a.idx != nullptr)
+    return fp8 ? launch_rows<true, true>(a, parts, err, st) : launch_rows<false, true>(a, parts, err, st);
+  return fp8 ? launch_rows<true, false>(a, parts, err, st) : launch_rows<false, false>(a, parts, err, st);
 }
 
 cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {
-  if (a.N <= 0) return cudaSuccess;
-  if (a.idx != nullptr)
-    return fp8 ? launch_rows<true, true>(a, ws, st) : launch_rows<false, true>(a, ws, st);
-  return fp8 ? launch_rows<true, false>(a, ws, st) : launch_rows<false, false>(a, ws, st);
+  return launch_paged_rows(a, fp8, static_cast<char*>(ws) + kRwHead, static_cast<int*>(ws), st);
 }
 
 // Chunks of few query rows per kv head go to the row kernel, which reads the
@@ -1121,13 +1147,33 @@ cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_
 // (E4M3 rows are converted for the tensor cores first, so they wait longer.)
 static bool use_rows(int fp8, int G, int max_q) { return (long long)max_q * G <= (fp8 ? 128 : 32); }
 
+// In a batch with a long chunk, sequences with one block of rows at most
+// (decoding ones, short drafts) go to the row kernel all the same: a tile of
+// 128 rows would be all but empty, and E4M3 rows would be converted for it.
+// Measured, us (with / without), 32 heads over 8, a chunk of 512 of 2K beside
+// 16 x 4K: E4M3 129 / 244, bf16 129 / 147; beside 63 x 4K: 244 / 741, 254 / 422.
+// Two launches more cost 6 to 10 us when there is no such sequence, so chunks
+// of 128 rows at most, which tend to be of one kind, go together (16 drafts of
+// 40 rows, bf16: 78 / 68).
+static int few_tokens(int B, int G, int max_q) { return B > 1 && (long long)max_q * G > 128 ? 16 / G : 0; }
+
 size_t paged_attn_workspace_bytes(int fp8, int B, int max_q, long long capacity, int Hkv, int G) {
-  return use_rows(fp8, G, max_q) ? paged_rows_workspace_bytes(fp8, B, Hkv, G, max_q)
-                            : paged_tc_workspace_bytes(fp8, B, Hkv, G, max_q, capacity);
+  if (use_rows(fp8, G, max_q)) return paged_rows_workspace_bytes(fp8, B, Hkv, G, max_q);
+  const int few = few_tokens(B, G, max_q);
+  return paged_tc_workspace_bytes(fp8, B, Hkv, G, max_q, capacity) +
+         (few ? paged_rows_part_bytes(fp8, B, Hkv, G, few) : 0);
 }
 
 cudaError_t launch_paged_attn(const PagedArgs& a, int fp8, void* ws, cudaStream_t st) {
-  return use_rows(fp8, a.G, a.max_q) ? launch_paged_rows(a, fp8, ws, st) : launch_paged_tc(a, fp8, ws, st);
+  if (use_rows(fp8, a.G, a.max_q)) return launch_paged_rows(a, fp8, ws, st);
+  PagedArgs part = a;
+  part.few = few_tokens(a.B, a.G, a.max_q);
+  cudaError_t e = launch_paged_tc(part, fp8, ws, st);
+  if (e != cudaSuccess || part.few == 0) return e;
+  part.max_q = part.many = part.few;
+  const long long capacity = (long long)a.max_pages << a.page_shift;
+  char* parts = static_cast<char*>(ws) + paged_tc_workspace_bytes(fp8, a.B, a.Hkv, a.G, a.max_q, capacity);
+  return launch_paged_rows(part, fp8, parts, static_cast<int*>(ws), st);
 }
 
 cudaError_t launch_paged_write(const uint16_t* k_new, const uint16_t* v_new, long long k_stride, long long v_stride,

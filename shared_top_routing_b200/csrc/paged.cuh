@@ -162,6 +162,7 @@ struct PagedArgs {
   const int32_t* table = nullptr;   // [B, max_pages]
   int B = 0, N = 0, max_q = 0, max_pages = 0, num_pages = 0, page_shift = 0;
   int Hq = 0, Hkv = 0, G = 0, k = 0;
+  int few = 0, many = 0x7fffffff;   // sequences of more than few (tensor cores) and at most many (rows) new tokens
   float qscale = 0.f;               // softmax scale * log2(e)
   uint16_t* out = nullptr;          // [N, Hq, 128]
   float* lse = nullptr;             // [N, Hq] or null
@@ -178,12 +179,15 @@ cudaError_t launch_paged_gather(const uint8_t* kp, const uint8_t* vp, const int3
                                 int k, int fp8, uint16_t* ko, uint16_t* vo, int* dbg, cudaStream_t st);
 // Attention of few query rows per kv head (idx set: one token per sequence
 // over selected rows; else a chunk of at most max_q tokens per sequence).
-size_t paged_rows_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q);
+// parts: partial results, paged_rows_part_bytes; err: the kernel error word.
+size_t paged_rows_part_bytes(int fp8, int B, int Hkv, int G, int max_q);
+size_t paged_rows_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q);   // the head with the word, and the parts
+cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* parts, int* err, cudaStream_t st);
 cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
 // Attention of many query rows per kv head on the tensor cores (paged_tc.cu).
 size_t paged_tc_workspace_bytes(int fp8, int B, int Hkv, int G, int max_q, long long capacity);
 cudaError_t launch_paged_tc(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
-// Chunk attention: picks the kernel for the chunk's length.
+// Chunk attention: picks the kernels for the chunks' lengths.
 size_t paged_attn_workspace_bytes(int fp8, int B, int max_q, long long capacity, int Hkv, int G);
 cudaError_t launch_paged_attn(const PagedArgs& a, int fp8, void* ws, cudaStream_t st);
 

@@ -126,7 +126,7 @@ struct TcItem {
 // Tokens of block qb, and the key tiles up to its last; 0 when it has none.
 __device__ __forceinline__ int item_span(const PagedArgs& a, const TcPlan& pl, int b, int qb, SeqSpan& s, int& nt) {
   s = seq_span(a.q_start, a.kv_len, b, a.N, a.max_pages << a.page_shift);
-  const int n = min(s.len, a.max_q), t0 = qb * pl.tpi;
+  const int n = s.len > a.few ? min(s.len, a.max_q) : 0, t0 = qb * pl.tpi;
   nt = min(pl.tpi, n - t0);
   if (nt <= 0) return 0;
   return max(1, (max(s.pos0 + t0 + nt, 0) + kTile - 1) / kTile);
@@ -955,10 +955,10 @@ paged_window_kernel(const PagedArgs a, const TcPlan pl, uint16_t* __restrict__ k
   const int rb = paged_row_bytes(1, a.Hkv), page_mask = (1 << a.page_shift) - 1;
   int skip = 0;   // positions before this sequence's, modulo the warps
   for (int g = 0; g < pl.nb; g += 32) {
-    int kv_of = 0;   // positions of sequence b0 + g + lane, if it has new tokens
+    int kv_of = 0;   // positions of sequence b0 + g + lane, if it is one of these
     if (g + lane < pl.nb) {
       const SeqSpan s = seq_span(a.q_start, a.kv_len, pl.b0 + g + lane, a.N, a.max_pages << a.page_shift);
-      kv_of = s.len > 0 ? s.kv : 0;
+      kv_of = s.len > a.few ? s.kv : 0;
     }
     for (int i = 0; i < min(32, pl.nb - g); ++i) {
       const int n = __shfl_sync(0xffffffffu, kv_of, i);

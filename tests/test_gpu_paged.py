@@ -457,6 +457,20 @@ def test_ragged_batches_of_many_items(kv_type, B, hkv, G):
 
 
 @pytest.mark.parametrize("kv_type", TYPES)
+@pytest.mark.parametrize("hkv,G", [(2, 1), (8, 4), (3, 5), (1, 16)])
+def test_decoding_sequences_beside_a_long_chunk(kv_type, hkv, G):
+    """Chunks of every length around a block of 16 rows, beside one of many;
+    tokens of no sequence around them, a sequence with nothing new."""
+    few = 16 // G
+    q_len = [1, few, 129 // G + 30, few + 1, 0, max(1, few - 1), 1]
+    kv = [70, few + 3, 250, 400, 5, 0, 1]
+    got, lse, ref, n = _attn_case(G, kv_type, hkv, G, 16, q_len, kv, lead=3, tail=40)
+    _check_attn(got, lse, ref, n)
+    dead = np.isnan(ref[1][:, 0])
+    assert dead.sum() == 43 and (got.float().cpu().numpy()[dead] == 7.0).all()
+
+
+@pytest.mark.parametrize("kv_type", TYPES)
 @pytest.mark.parametrize("lens", [[1000] * 4, [2000, 300, 77, 900]])
 def test_whole_prompts(kv_type, lens):
     """Items dealt to the CTAs whole, of one length and of many; every run the
