@@ -285,8 +285,8 @@ sa_status sa_sparse_attn_decode_rows(const void* q, const void* k_rows, const vo
  * New tokens of all sequences are packed: sequence b owns tokens
  * q_start[b] .. q_start[b + 1] - 1 (q_start [B + 1] int32, ascending, clamped
  * to [0, N] on the device), which are the LAST q_len = q_start[b + 1] -
- * q_start[b] of its kv_len[b] positions (kv_len [B] int32, clamped to
- * [0, max_pages * page_size]): token t sits at position kv_len[b] - q_len + t.
+ * q_start[b] of its kv_len[b] positions (kv_len [B] int32; attention clamps it
+ * to [0, max_pages * page_size]): token t sits at position kv_len[b] - q_len + t.
  * A sequence may have no new token.  Tokens before q_start[0] or from
  * q_start[B] on belong to no sequence: nothing is read or written for them.
  *

@@ -101,10 +101,11 @@ def paged_write(x_bits, pool, table, q_start, kv_len, kv_type: int) -> np.ndarra
     pool = pool.copy()
     num_pages, page_size, row = pool.shape
     flat = pool.reshape(-1, row)
-    for b, (a, n, kv) in enumerate(_spans(q_start, kv_len, x_bits.shape[0], table.shape[1] * page_size)):
+    capacity = table.shape[1] * page_size
+    for b, (a, n, _) in enumerate(_spans(q_start, kv_len, x_bits.shape[0], capacity)):
         for t in range(n):
-            pos = kv - n + t
-            if pos < 0:
+            pos = int(kv_len[b]) - n + t
+            if not 0 <= pos < capacity:
                 continue
             page = int(table[b, pos // page_size])
             if 0 <= page < num_pages:

@@ -139,8 +139,9 @@ paged_write_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restric
   if (b < 0) return;      // in front of the first sequence or behind the last
   const int capacity = max_pages << page_shift;
   const SeqSpan s = seq_span(q_start, kv_len, b, N, capacity);
-  const int pos = s.pos0 + (i - s.begin);
-  if (pos < 0) return;    // kv_len does not count this token: it has no place
+  const long long at = (long long)kv_len[b] - s.len + (i - s.begin);
+  if (at < 0 || at >= capacity) return;   // kv_len does not count this token, or the table has no place for it
+  const int pos = (int)at;
   const int pg = table[(long long)b * max_pages + (pos >> page_shift)];
   if (pg < 0 || pg >= num_pages) {   // no page: the token is dropped, no other page is touched
     if ((threadIdx.x & 31) == 0) paged_note(dbg, kDbgPage, pg, num_pages);
@@ -253,6 +254,9 @@ struct RowsPlan {
   bool by_item;            // merge: CTAs by row block and token, not by token (most tokens are not here)
 };
 
+// Tiles of R positions that hold n (n + R may pass 2^31).
+__device__ __forceinline__ int tiles_of(int n, int R) { return (int)(((unsigned)n + (unsigned)R - 1u) / (unsigned)R); }
+
 // Tiles of item p: the positions its last token attends to, or the selected
 // rows of its sequence.
 template <bool SPARSE>
@@ -269,7 +273,7 @@ __device__ __forceinline__ int item_keys(const PagedArgs& a, const RowsPlan& pl,
 }
 template <bool SPARSE>
 __device__ __forceinline__ int item_tiles(const PagedArgs& a, const RowsPlan& pl, int p) {
-  return (item_keys<SPARSE>(a, pl, p) + pl.R - 1) / pl.R;
+  return tiles_of(item_keys<SPARSE>(a, pl, p), pl.R);
 }
 
 // Sum over the block of v (threads kThreads, a multiple of 32), and the sum
@@ -658,7 +662,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
     bool ok = true;
     for (; left > 0 && ok; ++p, tile = 0) {
       const int keys = item_keys<SPARSE>(a, pl, p);
-      const int tiles = (keys + R - 1) / R;
+      const int tiles = tiles_of(keys, R);
       const int last = (int)min((long long)tiles, tile + left);
       if (tile >= last) continue;
       left -= last - tile;
@@ -778,7 +782,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
   bool ok = true;
   for (; left > 0 && ok; ++p, tile = 0) {
     const int keys = item_keys<SPARSE>(a, pl, p);
-    const int tiles = (keys + R - 1) / R;
+    const int tiles = tiles_of(keys, R);
     const int last = (int)min((long long)tiles, tile + left);
     if (tile >= last) continue;
     left -= last - tile;

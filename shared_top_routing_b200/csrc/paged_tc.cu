@@ -123,13 +123,18 @@ struct TcItem {
   __device__ __forceinline__ int first_masked() const { return pos0 < 0 ? 0 : (pos0 + 1) / kTile; }
 };
 
+// Key tiles below position end, one at least (end + kTile may pass 2^31).
+__device__ __forceinline__ int tiles_upto(int end) {
+  return max(1, (int)(((unsigned)max(end, 0) + (unsigned)kTile - 1u) / (unsigned)kTile));
+}
+
 // Tokens of block qb, and the key tiles up to its last; 0 when it has none.
 __device__ __forceinline__ int item_span(const PagedArgs& a, const TcPlan& pl, int b, int qb, SeqSpan& s, int& nt) {
   s = seq_span(a.q_start, a.kv_len, b, a.N, a.max_pages << a.page_shift);
   const int n = s.len > a.few ? min(s.len, a.max_q) : 0, t0 = qb * pl.tpi;
   nt = min(pl.tpi, n - t0);
   if (nt <= 0) return 0;
-  return max(1, (max(s.pos0 + t0 + nt, 0) + kTile - 1) / kTile);
+  return tiles_upto(s.pos0 + t0 + nt);
 }
 
 // Dealt items: CTA c's r-th, items from the longest to the shortest, kv heads
@@ -187,7 +192,7 @@ __device__ __forceinline__ bool next_item(const PagedArgs& a, const TcPlan& pl, 
     it.cntA = (len + 1) / 2;
     it.cntB = len / 2;
   } else {
-    const int nA = max(1, (max(it.pos0 + it.ntA, 0) + kTile - 1) / kTile);
+    const int nA = tiles_upto(it.pos0 + it.ntA);
     it.cntA = max(0, min(it.j1, nA) - it.j0);
     it.cntB = len;
   }
@@ -965,7 +970,7 @@ paged_window_kernel(const PagedArgs a, const TcPlan pl, uint16_t* __restrict__ k
       const int first = warp - skip + (warp < skip ? warps : 0);
       skip = (skip + n % warps) % warps;
       const int32_t* trow = a.table + (long long)(pl.b0 + g + i) * a.max_pages;
-      for (int pos = first; pos < n; pos += warps) {
+      for (unsigned pos = first; pos < (unsigned)n; pos += warps) {
         const int pg = checked_page(__ldg(trow + (pos >> a.page_shift)), a.num_pages, a.dbg);
         const long long off = (((long long)pg << a.page_shift) + (pos & page_mask)) * rb;
         const long long to = ((long long)(g + i) * pl.cap + pos) * pl.nh * kPgD;

@@ -126,6 +126,23 @@ def test_write(kv_type, hkv, page):
         assert not np.array_equal(ref, old)
 
 
+@pytest.mark.parametrize("kv_type", TYPES)
+def test_a_write_beyond_the_table_is_dropped(kv_type):
+    """Lengths past the table's last position, far past it and below zero: the
+    rows that have a place are written, every other byte stays."""
+    hkv, page, cols = 2, 16, 3
+    table = np.arange(4 * cols, dtype=np.int32)[::-1].reshape(4, cols).copy()
+    q_start, kv = [0, 5, 9, 12, 20], [page * cols + 2, 2 ** 31 - 1, -2 ** 31, page * cols]
+    x = _normal(40, 1, (20, hkv, 128))
+    old = _rng(41).integers(0, 256, (4 * cols, page, P.row_bytes(kv_type, hkv)), dtype=np.uint8)
+    pools = [_dev_pool(old, kv_type) for _ in range(2)]
+    sa.sa_paged_kv_write(to_dev(x), to_dev(x), *pools, i32(table), i32(q_start), i32(kv))
+    ref = P.paged_write(x, old, table, q_start, kv, kv_type)
+    assert (ref != old).reshape(4 * cols * page, -1).any(1).sum() == 3 + 8
+    for p in pools:
+        assert np.array_equal(_host_pool(p), ref)
+
+
 def test_write_values_at_the_ends_of_the_range():
     """Zeros, subnormals, the largest values, infinities, NaN, borders of the
     scale, ties of the codes."""
