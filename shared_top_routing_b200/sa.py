@@ -522,8 +522,9 @@ def _paged_workspace(nbytes: int, dev: int, raw_stream: int):
 
 
 def _paged_ws_args(L, size_of, sizes, ws, dev, raw):
-    """(pointer, bytes) of the call's workspace; its size is a function of the
-    call's sizes alone and is looked up once."""
+    """(pointer, bytes, tensor) of the call's workspace, the tensor to be held
+    until the launch; its size is a function of the call's sizes alone and is
+    looked up once."""
     key = (L._handle, dev, size_of, sizes)
     need = _paged_ws_need.get(key)
     if need is None:
@@ -532,11 +533,11 @@ def _paged_ws_args(L, size_of, sizes, ws, dev, raw):
         need = _paged_ws_need[key] = getattr(L, size_of)(*sizes)
     if ws is None:
         if need == 0:
-            return None, 0
+            return None, 0, None
         ws = _paged_workspace(need, dev, raw)
     elif ws.get_device() != dev:
         raise ValueError(f"ws must be on {_name(dev)}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def sa_paged_kv_write(k_new, v_new, k_pages, v_pages, block_table, q_start, kv_len, stream=None):
@@ -656,8 +657,8 @@ def _attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q, scale, out, 
     max_q = N if max_q is None else max_q
     out, lse = _outputs(q, shape, out, with_lse, dev)
     pages, page_size, _ = k_pages.shape
-    wp, wn = _paged_ws_args(L, "sa_paged_attn_workspace", (B, N, max_q, cols, page_size, Hq, Hkv, D, kv_type), ws, dev,
-                            raw)
+    wp, wn, ws = _paged_ws_args(L, "sa_paged_attn_workspace", (B, N, max_q, cols, page_size, Hq, Hkv, D, kv_type), ws,
+                                dev, raw)
     st = L.sa_paged_attn(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
                          q_start.data_ptr(), kv_len.data_ptr(), B, N, max_q, cols, pages, page_size, Hq, Hkv, D, kv_type,
                          scale, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wn, raw)
@@ -692,7 +693,7 @@ def _sparse(q, k_pages, v_pages, block_table, idx, count, scale, out, with_lse, 
     B, Hq, D = shape
     out, lse = _outputs(q, shape, out, with_lse, dev)
     pages, page_size, _ = k_pages.shape
-    wp, wn = _paged_ws_args(L, "sa_paged_sparse_attn_decode_workspace", (B, Hq, Hkv, D, k, kv_type), ws, dev, raw)
+    wp, wn, ws = _paged_ws_args(L, "sa_paged_sparse_attn_decode_workspace", (B, Hq, Hkv, D, k, kv_type), ws, dev, raw)
     st = L.sa_paged_sparse_attn_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
                                        idx.data_ptr(), count.data_ptr(), B, cols, pages, page_size, Hq, Hkv, D, k,
                                        kv_type, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wn,
