@@ -244,8 +244,8 @@ paged_gather_kernel(const uint8_t* __restrict__ kp, const uint8_t* __restrict__ 
 // ------------------------------------------------------- few-row attention
 
 constexpr int kRwConsumers = 8;
-// The producer has three idle warps beside it, whose registers the consumers
-// take (8 * 224 + 4 * 56 = 12 * 168; without: 121 us for one token of each of
+// The producer and the three warps beside it (which copy selected rows and are
+// idle otherwise) leave registers to the consumers (8 * 224 + 4 * 56 = 12 * 168; without: 121 us for one token of each of
 // 8 x 32K E4M3 positions, 115 with).
 constexpr int kRwThreads = (kRwConsumers + 4) * 32, kRwConsumerRegs = 224, kRwOtherRegs = 56;
 constexpr int kRwMaxStages = 8;
@@ -317,6 +317,23 @@ __device__ __forceinline__ long long block_scan(int v, long long& before, long l
   }
   before = base + x - v;
   return total;
+}
+
+// v, and the sum over the lanes before this one; returns the warp's.
+__device__ __forceinline__ long long warp_scan(int v, long long& before) {
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((int)(threadIdx.x & 31) >= o) x += y;
+  }
+  before = x - v;
+  return __shfl_sync(0xffffffffu, x, 31);
+}
+
+// floor(x / d), x >= 0, d > 0 (a division of 64 bits takes hundreds of clocks).
+__device__ __forceinline__ long long floor_div(long long x, long long d) {
+  return (unsigned long long)(x | d) >> 32 ? x / d : (long long)((unsigned)x / (unsigned)d);
 }
 
 // Query fragments (the M side): row r of the block is token t0 + r / G, head
@@ -643,40 +660,56 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
 
   // ---- the CTA's share [lo, hi) of all tiles, and where it starts
-  const int per = (pl.P + kRwThreads - 1) / kRwThreads;
-  const int p0 = min((int)threadIdx.x * per, pl.P), p1 = min(p0 + per, pl.P);
-  int mine = 0;
-  for (int p = p0; p < p1; ++p) mine += item_tiles<SPARSE>(a, pl, p);
-  long long before;
-  const long long U = block_scan<kRwThreads>(mine, before, sh_scan);
-  const long long Weff = U < pl.W ? U : pl.W;
-  if ((long long)blockIdx.x >= Weff) return;   // fewer tiles than CTAs
-  const long long lo = blockIdx.x * U / Weff, hi = (blockIdx.x + 1) * U / Weff;
-  if (before <= lo && lo < before + mine) {
-    long long at = before;
-    for (int p = p0; p < p1; ++p) {
-      const int n = item_tiles<SPARSE>(a, pl, p);
-      if (lo < at + n) {
-        sh_plan[0] = p;
-        sh_plan[1] = (int)(lo - at);
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
   const int capacity = a.max_pages << a.page_shift;
-  int p = sh_plan[0], tile = sh_plan[1];
-  long long left = hi - lo;
+  int p, tile;
+  long long left;
+  if (pl.P <= 32) {   // every warp works it out by itself
+    const int n = lane < pl.P ? item_tiles<SPARSE>(a, pl, lane) : 0;
+    long long before;
+    const long long U = warp_scan(n, before), Weff = U < pl.W ? U : pl.W;
+    if ((long long)blockIdx.x >= Weff) return;   // fewer tiles than CTAs
+    const long long lo = floor_div(blockIdx.x * U, Weff);
+    left = floor_div((blockIdx.x + 1) * U, Weff) - lo;
+    p = __ffs(__ballot_sync(0xffffffffu, before <= lo && lo < before + n)) - 1;
+    tile = (int)(lo - __shfl_sync(0xffffffffu, before, p));
+  } else {
+    const int per = (pl.P + kRwThreads - 1) / kRwThreads;
+    const int p0 = min((int)threadIdx.x * per, pl.P), p1 = min(p0 + per, pl.P);
+    int mine = 0;
+    for (int i = p0; i < p1; ++i) mine += item_tiles<SPARSE>(a, pl, i);
+    long long before;
+    const long long U = block_scan<kRwThreads>(mine, before, sh_scan), Weff = U < pl.W ? U : pl.W;
+    if ((long long)blockIdx.x >= Weff) return;
+    const long long lo = floor_div(blockIdx.x * U, Weff);
+    left = floor_div((blockIdx.x + 1) * U, Weff) - lo;
+    if (before <= lo && lo < before + mine) {
+      long long at = before;
+      for (int i = p0; i < p1; ++i) {
+        const int n = per == 1 ? mine : item_tiles<SPARSE>(a, pl, i);
+        if (lo < at + n) {
+          sh_plan[0] = i;
+          sh_plan[1] = (int)(lo - at);
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    p = sh_plan[0], tile = sh_plan[1];
+  }
 
   if (warp >= kRwConsumers) {
     // ------------------------------------------------------------ producer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRwOtherRegs));
-    if (warp > kRwConsumers) return;   // (registers are split by four warps)
+    // pages are copied by one warp, selected rows by four: a warp issues a copy
+    // every 55 clocks or so (8 x 2048 rows, E4M3: 22.3 us by one, 15.3 by four)
+    const int pw = warp - kRwConsumers;
+    if (!SPARSE && pw > 0) return;
     uint32_t fill = 0;
     const int page_mask = (1 << a.page_shift) - 1;
     bool ok = true;
@@ -694,17 +727,19 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
       // tile's copies are issued
       int e0 = 0, pg = 0, pg_next = 0;
       const int e_last = SPARSE ? 0 : (keys - 1) >> a.page_shift;
-      constexpr int NI = kRwKeys<FP8> / 4;   // rows per lane: a tile has at most 8 slices
+      constexpr int NI = kRwKeys<FP8> / 8;   // copies per lane: a tile has at most 8 slices
       int jn[NI] = {}, pn[NI] = {}, jnn[NI] = {};
       const int32_t* irow = SPARSE ? a.idx + (long long)b * a.k : nullptr;
+      // copy c of a tile: row c / 2, of K or V
+      auto row_of = [&](int i) { return (lane * 4 + pw + 128 * i) >> 1; };
       auto load_idx = [&](int (&j)[NI], int t) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const int r = lane + 32 * i, at = t * R + r;
+          const int r = row_of(i), at = t * R + r;
           if (r < R && at < keys) {
             int v = __ldg(irow + at);
             if (v < 0 || v >= capacity) {
-              paged_note(a.dbg, kDbgPagedIndex, v, capacity);
+              if ((pw & 1) == 0) paged_note(a.dbg, kDbgPagedIndex, v, capacity);
               v = v < 0 ? 0 : capacity - 1;
             }
             j[i] = v;
@@ -714,7 +749,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
       auto load_pages = [&](int (&g)[NI], const int (&j)[NI], int t) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const int r = lane + 32 * i;
+          const int r = row_of(i);
           if (r < R && t * R + r < keys) g[i] = __ldg(trow + (j[i] >> a.page_shift));
         }
       };
@@ -737,7 +772,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
         unsigned char* stK = ring + (size_t)s * stage_bytes;
         unsigned char* stV = stK + (size_t)R * rb;
         const int rows = min(R, keys - t * R);   // rows past the last key stay as they are (masked)
-        if (lane == 0) tc::mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)rows * (uint32_t)rb);
+        if (pw == 0 && lane == 0) tc::mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)rows * (uint32_t)rb);
         __syncwarp();
         if constexpr (SPARSE) {
           int jc[NI], pc[NI];
@@ -747,12 +782,12 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
           if (t + 2 < last) load_idx(jnn, t + 2);
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
-            const int r = lane + 32 * i;
+            const int r = row_of(i);
             if (r < rows) {
-              const int page = checked_page(pc[i], a.num_pages, a.dbg);
+              const int page = checked_page(pc[i], a.num_pages, pw & 1 ? nullptr : a.dbg);
               const long long off = (((long long)page << a.page_shift) + (jc[i] & page_mask)) * rb;
-              tc::bulk_load(stK + (size_t)r * rb, a.kp + off, (uint32_t)rb, &full[s]);
-              tc::bulk_load(stV + (size_t)r * rb, a.vp + off, (uint32_t)rb, &full[s]);
+              if (pw & 1) tc::bulk_load(stV + (size_t)r * rb, a.vp + off, (uint32_t)rb, &full[s]);
+              else tc::bulk_load(stK + (size_t)r * rb, a.kp + off, (uint32_t)rb, &full[s]);
             }
           }
         } else {
@@ -781,7 +816,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
       }
     }
     // every copy this CTA issued lands before it exits
-    for (int s = 0; s < pl.stages; ++s) {
+    for (int s = 0; s < pl.stages && pw == 0; ++s) {
       if ((uint32_t)s < fill) {
         const uint32_t last_use = (fill - 1 - (uint32_t)s) / (uint32_t)pl.stages;
         if (!tc::mbar_wait_drain(&full[s], last_use & 1u) && err) atomicCAS(err, 0, 22);
@@ -896,42 +931,60 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
     tok = s.begin + t;
   }
   // the token's item, the tiles before it and in all
-  if (tid == 0) sh_item[0] = -1;
-  const int per = (pl.P + kRwMergeThreads - 1) / kRwMergeThreads;
-  const int p0 = min(tid * per, pl.P), p1 = min(p0 + per, pl.P);
-  int mine = 0, hit = -1, hit_at = 0, hit_n = 0, hit_row = 0;
-  for (int i = p0; i < p1; ++i) {
-    const int n = item_tiles<SPARSE>(a, pl, i);
-    bool here = i == (SPARSE ? tok : p_by);
-    int t = t_by;
-    if (!SPARSE && !pl.by_item) {
-      const SeqSpan s = seq_span(a.q_start, a.kv_len, i / pl.nrb, a.N, a.max_pages << a.page_shift);
-      t = tok - s.begin - i % pl.nrb * pl.tb;
-      here = t >= 0 && t < pl.tb && t + i % pl.nrb * pl.tb < min(s.len, a.max_q);
+  auto holds = [&](int i, int& t) {   // whether item i holds the token, as its t-th
+    t = t_by;
+    if (SPARSE || pl.by_item) return i == (SPARSE ? tok : p_by);
+    const SeqSpan s = seq_span(a.q_start, a.kv_len, i / pl.nrb, a.N, a.max_pages << a.page_shift);
+    const int t0 = i % pl.nrb * pl.tb;
+    t = tok - s.begin - t0;
+    return t >= 0 && t < pl.tb && t + t0 < min(s.len, a.max_q);
+  };
+  int p = -1, n_p = 0, t_p = 0;
+  long long U, base_u = 0;
+  if (pl.P <= 32) {   // every warp works it out by itself
+    const int n = lane < pl.P ? item_tiles<SPARSE>(a, pl, lane) : 0;
+    int t;
+    const uint32_t hit = __ballot_sync(0xffffffffu, lane < pl.P && holds(lane, t));
+    long long before;
+    U = warp_scan(n, before);
+    if (hit) {
+      p = __ffs(hit) - 1;
+      n_p = __shfl_sync(0xffffffffu, n, p);
+      t_p = __shfl_sync(0xffffffffu, t, p);
+      base_u = __shfl_sync(0xffffffffu, before, p);
     }
-    if (here) hit = i, hit_at = mine, hit_n = n, hit_row = t * a.G;
-    mine += n;
+  } else {
+    if (tid == 0) sh_item[0] = -1;
+    const int per = (pl.P + kRwMergeThreads - 1) / kRwMergeThreads;
+    const int p0 = min(tid * per, pl.P), p1 = min(p0 + per, pl.P);
+    int mine = 0, mine_at = 0;
+    for (int i = p0; i < p1; ++i) {
+      const int n = item_tiles<SPARSE>(a, pl, i);
+      int t;
+      if (holds(i, t)) p = i, n_p = n, t_p = t, mine_at = mine;
+      mine += n;
+    }
+    long long before;
+    U = block_scan<kRwMergeThreads>(mine, before, sh_scan);
+    if (p >= 0) {
+      sh_item[0] = p;
+      sh_item[1] = n_p;
+      sh_item[2] = t_p;
+      sh_at = before + mine_at;
+    }
+    __syncthreads();
+    p = sh_item[0], n_p = sh_item[1], t_p = sh_item[2];
+    base_u = sh_at;
   }
-  long long before;
-  const long long U = block_scan<kRwMergeThreads>(mine, before, sh_scan);
-  if (hit >= 0) {
-    sh_item[0] = hit;
-    sh_item[1] = hit_n;
-    sh_item[2] = hit_row;
-    sh_at = before + hit_at;
-  }
-  __syncthreads();
-  const int p = sh_item[0], n_p = sh_item[1];
   if (p < 0) {   // of no sequence, or beyond the bound
     pdl_wait();
     return;
   }
-  const int hs = min(h, a.Hq - 1) / a.G, row = sh_item[2] + h % a.G;
-  const long long base_u = sh_at;
+  const int hs = min(h, a.Hq - 1) / a.G, row = t_p * a.G + h % a.G;
   const long long Weff = U < pl.W ? U : pl.W;
   // the CTA that owns unit u: the largest c with floor(c U / W) <= u
-  const long long first = n_p ? ((base_u + 1) * Weff - 1) / U : 0;
-  const long long last_c = n_p ? ((base_u + n_p) * Weff - 1) / U : -1;
+  const long long first = n_p ? floor_div((base_u + 1) * Weff - 1, U) : 0;
+  const long long last_c = n_p ? floor_div((base_u + n_p) * Weff - 1, U) : -1;
   const int C = (int)(last_c - first + 1) * pl.wph;
   const long long xstride = (long long)a.Hkv * pl.RB;   // entries between consecutive contributors
   const long long e0 = (((long long)p + first) * pl.wph * a.Hkv + hs) * pl.RB + row;
