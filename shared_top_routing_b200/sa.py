@@ -426,16 +426,29 @@ def sa_paged_kv_alloc(num_pages: int, page_size: int, Hkv: int, kv_type: int = S
 
 
 # The checks below run on every call of a decode step, so they are written for
-# few interpreter steps: devices as ordinals, one tuple comparison per shape.
+# few interpreter steps: devices as ordinals, one tuple comparison per shape,
+# torch's names looked up once.  Of the ways to allocate, empty_like and
+# empty_strided take the least time.
+
+_bf16 = _u8 = _i32 = _f32 = _cuda = _empty_like = _empty_strided = None
+
+
+def _names():
+    global _bf16, _u8, _i32, _f32, _cuda, _empty_like, _empty_strided
+    torch = _torch()
+    _u8, _i32, _f32, _cuda = torch.uint8, torch.int32, torch.float32, torch._C
+    _empty_like, _empty_strided, _bf16 = torch.empty_like, torch.empty_strided, torch.bfloat16
+
 
 def _pools(k_pages, v_pages, dev):
     """(kv_type, Hkv) of a pair of pools on CUDA device `dev` (an ordinal): by
     their element type and row size."""
-    torch = _torch()
+    if _bf16 is None:
+        _names()
     dtype, shape = k_pages.dtype, k_pages.shape
-    if dtype is torch.bfloat16:
+    if dtype is _bf16:
         kv_type, pad = SA_KV_BF16, 8
-    elif dtype is torch.uint8:
+    elif dtype is _u8:
         kv_type, pad = SA_KV_E4M3, 16
     else:
         raise ValueError("k_pages must be bfloat16, or uint8 for E4M3 rows")
@@ -456,7 +469,7 @@ def _name(dev):
 
 
 def _ints32(t, name, dev, shape):
-    if t.dtype is not _torch().int32 or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not (_i32 or _torch().int32) or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor on {_name(dev)}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, has {list(t.shape)}")
@@ -465,8 +478,10 @@ def _ints32(t, name, dev, shape):
 def _tokens(t, name):
     """(device ordinal, shape, token stride) of [N, H, 128] bf16 rows whose
     heads lie side by side."""
+    if _bf16 is None:
+        _names()
     dev = t.get_device()
-    if dev < 0 or t.dtype is not _torch().bfloat16:
+    if dev < 0 or t.dtype is not _bf16:
         raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
     shape = t.shape
     if len(shape) != 3:
@@ -490,13 +505,12 @@ def _call_stream(dev, stream):
     the given stream, or the current one of that device.  The context makes
     the device (and a given stream, so that outputs belong to it) current;
     None when they are already."""
-    torch = _torch()
     if stream is not None:
         if stream.device.index != dev:
             raise ValueError(f"the stream is of {stream.device}, the tensors are on {_name(dev)}")
-        return stream.cuda_stream, torch.cuda.stream(stream)
-    raw = torch._C._cuda_getCurrentRawStream(dev)
-    return raw, None if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
+        return stream.cuda_stream, _torch().cuda.stream(stream)
+    raw = _cuda._cuda_getCurrentRawStream(dev)
+    return raw, None if _cuda._cuda_getDevice() == dev else _torch().cuda.device(dev)
 
 
 _paged_ws: dict = {}
@@ -508,15 +522,14 @@ def _paged_workspace(nbytes: int, dev: int, raw_stream: int):
     a capture, one buffer per stream is kept and grows.  A capture gets a
     buffer of its own from the graph's memory, zeroed by the graph, so that
     graphs share none with each other or with calls outside."""
-    torch = _torch()
-    if torch._C._cuda_isCurrentStreamCapturing():
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    if _cuda._cuda_isCurrentStreamCapturing():
+        buf = _torch().empty(nbytes, dtype=_u8, device=f"cuda:{dev}")
         buf[:SA_WS_ALIGN].zero_()
         return buf
     key = (dev, raw_stream)
     buf = _paged_ws.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+        buf = _torch().zeros(nbytes, dtype=_u8, device=f"cuda:{dev}")
         _paged_ws[key] = buf
     return buf
 
@@ -535,7 +548,8 @@ def _paged_ws_args(L, size_of, sizes, ws, dev, raw):
         if need == 0:
             return None, 0, None
         ws = _paged_workspace(need, dev, raw)
-    elif ws.get_device() != dev:
+        return ws.data_ptr(), need, ws
+    if ws.get_device() != dev:
         raise ValueError(f"ws must be on {_name(dev)}")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
@@ -549,6 +563,7 @@ def sa_paged_kv_write(k_new, v_new, k_pages, v_pages, block_table, q_start, kv_l
     dev, kshape, ks = _tokens(k_new, "k_new")
     vdev, vshape, vs = _tokens(v_new, "v_new")
     kv_type, Hkv = _pools(k_pages, v_pages, dev)
+    pages, page_size, _ = k_pages.shape
     N = kshape[0]
     if kshape != (N, Hkv, _D) or vshape != kshape or vdev != dev:
         raise ValueError(f"k_new and v_new must have shape [N, {Hkv}, {_D}], on one device")
@@ -556,7 +571,6 @@ def sa_paged_kv_write(k_new, v_new, k_pages, v_pages, block_table, q_start, kv_l
     _ints32(q_start, "q_start", dev, (B + 1,))
     _ints32(kv_len, "kv_len", dev, (B,))
     raw, ctx = _call_stream(dev, stream)
-    pages, page_size, _ = k_pages.shape
     args = (k_new.data_ptr(), v_new.data_ptr(), ks, vs, q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), B,
             N, cols, pages, page_size, Hkv, _D, kv_type, k_pages.data_ptr(), v_pages.data_ptr(), raw)
     if ctx is None:
@@ -573,7 +587,8 @@ def _table(block_table, dev):
     shape = block_table.shape
     if len(shape) != 2:
         raise ValueError("block_table must have shape [B, max_pages]")
-    _ints32(block_table, "block_table", dev, shape)
+    if block_table.dtype is not _i32 or block_table.get_device() != dev or not block_table.is_contiguous():
+        _ints32(block_table, "block_table", dev, shape)   # (says what is wrong)
     return shape
 
 
@@ -592,6 +607,7 @@ def sa_paged_kv_gather(k_pages, v_pages, block_table, idx, count, k_rows=None, v
     (zeros past count), for sa_sparse_attn_decode_rows.  idx [B, k], count [B]."""
     dev = k_pages.get_device()
     kv_type, Hkv = _pools(k_pages, v_pages, dev)
+    pages, page_size, _ = k_pages.shape
     B, cols = _table(block_table, dev)
     k = _selection(idx, count, B, dev)
     if dev < 0:
@@ -599,16 +615,23 @@ def sa_paged_kv_gather(k_pages, v_pages, block_table, idx, count, k_rows=None, v
     raw, ctx = _call_stream(dev, stream)
     if ctx is not None:
         with ctx:
-            return _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, Hkv, B, cols, k, dev, raw)
-    return _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, Hkv, B, cols, k, dev, raw)
+            return _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, Hkv, pages, page_size, B,
+                           cols, k, dev, raw)
+    return _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, Hkv, pages, page_size, B, cols, k,
+                   dev, raw)
 
 
-def _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, Hkv, B, cols, k, dev, raw):
-    bf16 = _torch().bfloat16
-    shape = (B, k, Hkv * _D + 8)
-    k_rows = k_pages.new_empty(shape, dtype=bf16) if k_rows is None else _result(k_rows, "k_rows", dev, shape, bf16)
-    v_rows = k_pages.new_empty(shape, dtype=bf16) if v_rows is None else _result(v_rows, "v_rows", dev, shape, bf16)
-    pages, page_size, _ = k_pages.shape
+def _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, Hkv, pages, page_size, B, cols, k, dev,
+            raw):
+    row = Hkv * _D + 8
+    shape = (B, k, row)
+
+    def rows(t, name):
+        if t is None:
+            return _empty_strided(shape, (k * row, row, 1), dtype=_bf16, device=k_pages.device)
+        return _result(t, name, dev, shape, _bf16)
+
+    k_rows, v_rows = rows(k_rows, "k_rows"), rows(v_rows, "v_rows")
     st = lib().sa_paged_kv_gather(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), idx.data_ptr(),
                                   count.data_ptr(), B, cols, pages, page_size, Hkv, _D, k, kv_type, k_rows.data_ptr(),
                                   v_rows.data_ptr(), raw)
@@ -618,14 +641,14 @@ def _gather(k_pages, v_pages, block_table, idx, count, k_rows, v_rows, kv_type, 
 
 def _outputs(q, shape, out, with_lse, dev):
     """(out, lse or None) of queries q [N, Hq, 128]."""
-    torch = _torch()
+    N, Hq, D = shape
     if out is not None:
-        _result(out, "out", dev, shape, torch.bfloat16)
+        _result(out, "out", dev, shape, _bf16)
     elif q.is_contiguous():
-        out = torch.empty_like(q)
+        out = _empty_like(q)
     else:
-        out = q.new_empty(shape)
-    return out, q.new_empty(shape[:2], dtype=torch.float32) if with_lse else None
+        out = _empty_strided(shape, (Hq * D, D, 1), dtype=_bf16, device=q.device)
+    return out, _empty_strided((N, Hq), (Hq, 1), dtype=_f32, device=q.device) if with_lse else None
 
 
 def sa_paged_attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q: int | None = None, scale: float = 0.0,
@@ -638,6 +661,7 @@ def sa_paged_attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q: int 
     decode; by default N).  Returns out [N, Hq, 128][, lse [N, Hq] fp32]."""
     dev, shape, qs = _tokens(q, "q")
     kv_type, Hkv = _pools(k_pages, v_pages, dev)
+    pages, page_size, _ = k_pages.shape
     B, cols = _table(block_table, dev)
     _ints32(q_start, "q_start", dev, (B + 1,))
     _ints32(kv_len, "kv_len", dev, (B,))
@@ -645,18 +669,17 @@ def sa_paged_attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q: int 
     if ctx is not None:
         with ctx:
             return _attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q, scale, out, with_lse, ws, dev, shape,
-                         qs, kv_type, Hkv, B, cols, raw)
+                         qs, kv_type, Hkv, pages, page_size, B, cols, raw)
     return _attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q, scale, out, with_lse, ws, dev, shape, qs,
-                 kv_type, Hkv, B, cols, raw)
+                 kv_type, Hkv, pages, page_size, B, cols, raw)
 
 
 def _attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q, scale, out, with_lse, ws, dev, shape, qs, kv_type,
-          Hkv, B, cols, raw):
+          Hkv, pages, page_size, B, cols, raw):
     L = lib()
     N, Hq, D = shape
     max_q = N if max_q is None else max_q
     out, lse = _outputs(q, shape, out, with_lse, dev)
-    pages, page_size, _ = k_pages.shape
     wp, wn, ws = _paged_ws_args(L, "sa_paged_attn_workspace", (B, N, max_q, cols, page_size, Hq, Hkv, D, kv_type), ws,
                                 dev, raw)
     st = L.sa_paged_attn(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
@@ -674,6 +697,7 @@ def sa_paged_sparse_attn_decode(q, k_pages, v_pages, block_table, idx, count, sc
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     kv_type, Hkv = _pools(k_pages, v_pages, dev)
+    pages, page_size, _ = k_pages.shape
     B, cols = _table(block_table, dev)
     if shape[0] != B:
         raise ValueError(f"q must have shape [{B}, heads, {_D}]: one token per sequence")
@@ -682,17 +706,17 @@ def sa_paged_sparse_attn_decode(q, k_pages, v_pages, block_table, idx, count, sc
     if ctx is not None:
         with ctx:
             return _sparse(q, k_pages, v_pages, block_table, idx, count, scale, out, with_lse, ws, dev, shape, kv_type,
-                           Hkv, cols, k, raw)
+                           Hkv, pages, page_size, cols, k, raw)
     return _sparse(q, k_pages, v_pages, block_table, idx, count, scale, out, with_lse, ws, dev, shape, kv_type, Hkv,
-                   cols, k, raw)
+                   pages, page_size, cols, k, raw)
 
 
-def _sparse(q, k_pages, v_pages, block_table, idx, count, scale, out, with_lse, ws, dev, shape, kv_type, Hkv, cols, k,
+def _sparse(q, k_pages, v_pages, block_table, idx, count, scale, out, with_lse, ws, dev, shape, kv_type, Hkv, pages,
+            page_size, cols, k,
             raw):
     L = lib()
     B, Hq, D = shape
     out, lse = _outputs(q, shape, out, with_lse, dev)
-    pages, page_size, _ = k_pages.shape
     wp, wn, ws = _paged_ws_args(L, "sa_paged_sparse_attn_decode_workspace", (B, Hq, Hkv, D, k, kv_type), ws, dev, raw)
     st = L.sa_paged_sparse_attn_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
                                        idx.data_ptr(), count.data_ptr(), B, cols, pages, page_size, Hq, Hkv, D, k,
