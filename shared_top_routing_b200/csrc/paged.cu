@@ -13,7 +13,8 @@
 // maximum and sum.  It reads the cache once, 2 * row bytes per position for
 // 4 * 128 * Hq flops, so it is bound by HBM; the row side of the matrix
 // instructions (mma.sync, 16 rows) holds the G query heads of the chunk's
-// tokens, which share the kv head's rows.
+// tokens, which share the kv head's rows; with 8 rows at most the keys take
+// that side.
 //
 //   paged_write_kernel       one warp per token (K and V)
 //   paged_gather_kernel      one warp per selected row (K and V)
@@ -434,15 +435,14 @@ constexpr float kRwLift = 9.f, kRwLazy = 6.f;
 // sum, output.  tK, tV: the slice's first row, this kv head; rb: bytes from
 // row to row; sK, sV: the scale bytes of this head in the slice's first row.
 // Key rbase + i is seen by row r when it is <= lim[r] (-1: never).
-// HALF: rows 8 to 15 do not exist (their weights are 0).
 // EDGE: some key of the slice is not seen by some row.  Then V rows that no
 // row sees are zeroed, and infinities and NaN in V are taken out of the
 // product and added to the rows that see them only.
-template <bool FP8, bool EDGE, bool HALF>
+template <bool FP8, bool EDGE>
 __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4], const float (&rowc)[2],
                                          const uint8_t* tK, const uint8_t* tV, int rb, const uint8_t* sK,
                                          const uint8_t* sV, int rbase, const int (&lim)[2], int top) {
-  constexpr int KS = kRwKeys<FP8>, NT = KS / 8, NH = HALF ? 1 : 2, NE = 2 * NH;
+  constexpr int KS = kRwKeys<FP8>, NT = KS / 8, NH = 2, NE = 4;
   const int lane = threadIdx.x & 31, tg = lane & 3, mtx = lane >> 3;
   float sc[NT][4];
 #pragma unroll
@@ -564,10 +564,8 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
     for (int dt = 0; dt < 16; ++dt) {
       st.o[dt][0] *= alpha[0];
       st.o[dt][1] *= alpha[0];
-      if (!HALF) {
-        st.o[dt][2] *= alpha[1];
-        st.o[dt][3] *= alpha[1];
-      }
+      st.o[dt][2] *= alpha[1];
+      st.o[dt][3] *= alpha[1];
     }
   }
   bool bad = false;
@@ -633,6 +631,192 @@ __device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4
           if constexpr (FP8) x = (row[d] & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
           else x = bf_lo(reinterpret_cast<const uint16_t*>(row)[d]);
           if (!isfinite(x) && rbase + i <= lim[e >> 1]) st.o[dt][e] += x;
+        }
+    }
+  }
+}
+
+// An 8 x 8 block of 16-bit values, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// row_step for blocks of at most 8 rows, with the keys (then the output's
+// elements) on the 16-row side of the products and the query rows on the
+// 8-column side: half as many products as with 8 of 16 rows empty (E4M3, one
+// token of each of 8 x 32K positions 95 us for 97, of 8 x 2048 selected ones
+// 14.4 for 15.4).  A lane holds
+// rows 2 tg + {0, 1} and, of every 16 keys, gq and gq + 8; its parts of a
+// row's sum are added up at the end, and no lane needs another's maximum
+// until a reference rises.  st.o[c][e]: row 2 tg + (e & 1), element
+// 16 c + 2 gq + (e >> 1) (codes) or 16 c + 8 (e >> 1) + gq.
+template <bool FP8, bool EDGE>
+__device__ __forceinline__ void row_step_few(RowState& st, const uint32_t (&qa)[8][4], const float (&rowc)[2],
+                                             const uint8_t* tK, const uint8_t* tV, int rb, const uint8_t* sK,
+                                             const uint8_t* sV, int rbase, const int (&lim)[2], int top) {
+  constexpr int KS = kRwKeys<FP8>, KH = KS / 16;
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tg = lane & 3, mtx = lane >> 3;
+  float sc[KH][4], sd[KH][4];
+#pragma unroll
+  for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[kh][e] = sd[kh][e] = 0.f;
+  const uint8_t* kr = tK + ((mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
+  float kscale[KH][2], vexp[KH][2];
+  if constexpr (FP8) {
+#pragma unroll
+    for (int c = 0; c < 8; c += 2)
+#pragma unroll
+      for (int kh = 0; kh < KH; ++kh) {   // 16 keys x 32 codes
+        uint32_t w[4];                    // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
+        ldmatrix_x4(w[0], w[1], w[2], w[3], kr + kh * 16 * rb + c * 16);
+        uint32_t a[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], a[i >> 1][i & 1], a[i >> 1][2 + (i & 1)]);
+        mma_f16_16816(sc[kh], a[0], qa[c][0], qa[c][2]);
+        mma_f16_16816(sd[kh], a[1], qa[c + 1][0], qa[c + 1][2]);
+      }
+    // lane l converts the scales of key l; each lane takes those of its keys
+    const float ks = e8m0_value(sK[lane * rb]), ve = e8m0_exponent(sV[lane * rb]);
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        kscale[kh][h] = __shfl_sync(0xffffffffu, ks, kh * 16 + h * 8 + gq);
+        vexp[kh][h] = __shfl_sync(0xffffffffu, ve, kh * 16 + h * 8 + gq);
+      }
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < 8; kk += 2) {
+      uint32_t a[4], b[4];   // keys 0-7 and 8-15, first and last 8 of 16 elements
+      ldmatrix_x4(a[0], a[1], a[2], a[3], kr + kk * 32);
+      ldmatrix_x4(b[0], b[1], b[2], b[3], kr + kk * 32 + 32);
+      mma_bf16_16816(sc[0], a, qa[kk][0], qa[kk][2]);
+      mma_bf16_16816(sd[0], b, qa[kk + 1][0], qa[kk + 1][2]);
+    }
+  }
+  // base-2 logits; masked ones are -inf whatever the product was
+  float mx[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = e & 1, h = e >> 1;
+      float z = (sc[kh][e] + sd[kh][e]) * rowc[row];
+      if constexpr (FP8) z *= kscale[kh][h];
+      if (EDGE) z = rbase + kh * 16 + h * 8 + gq <= lim[row] ? z : -INFINITY;
+      sc[kh][e] = z;
+      mx[row] = fmaxf(mx[row], z);
+      // (an exponent that is NaN makes the weight NaN, not the reference)
+      if constexpr (FP8) mv[row] = fmaxf(mv[row], z + vexp[kh][h]);
+    }
+  bool up = false;
+#pragma unroll
+  for (int row = 0; row < 2; ++row) {
+    up |= mx[row] > st.m[row] + kRwLazy;
+    if constexpr (FP8) up |= mv[row] > st.mo[row] + kRwLazy;
+  }
+  if (__any_sync(0xffffffffu, up)) {   // a reference rises
+    float alpha[2];
+#pragma unroll
+    for (int row = 0; row < 2; ++row) {
+      alpha[row] = 1.f;
+      float v = mx[row], u = mv[row];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if constexpr (FP8) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+      }
+      if (v > st.m[row] + kRwLazy) {
+        alpha[row] = ex2(st.m[row] - v);
+        st.m[row] = v;
+        st.l[row] *= alpha[row];
+      }
+      if constexpr (FP8) {   // the output's own reference
+        alpha[row] = 1.f;
+        if (u > st.mo[row] + kRwLazy) {
+          alpha[row] = ex2(st.mo[row] - u);
+          st.mo[row] = u;
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.o[c][e] *= alpha[e & 1];
+  }
+  float mu[2], mo[2];
+#pragma unroll
+  for (int row = 0; row < 2; ++row) {
+    mu[row] = st.m[row] == -INFINITY ? 0.f : st.m[row];
+    mo[row] = (st.mo[row] == -INFINITY ? 0.f : st.mo[row]) - kRwLift;
+  }
+  bool bad = false;
+#pragma unroll
+  for (int kh = 0; kh < KH; ++kh) {
+    uint32_t pb[2];   // weights of 8 keys x 8 rows, then as the products want them
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float wt[2];
+#pragma unroll
+      for (int row = 0; row < 2; ++row) {
+        const float z = sc[kh][2 * h + row];
+        wt[row] = ex2(z - mu[row]);
+        st.l[row] += wt[row];
+        if constexpr (FP8) {
+          float zo = z + vexp[kh][h];
+          if (EDGE) zo = z == -INFINITY ? -INFINITY : zo;   // (a masked row's scale may be NaN)
+          wt[row] = ex2(zo - mo[row]);
+        }
+      }
+      pb[h] = transpose_8x8(FP8 ? pack_f16x2(wt[0], wt[1]) : pack_bf16x2(wt[0], wt[1]));
+    }
+    // V fragment registers hold keys 2 tg, 2 tg + 1 and those + 8
+    const int k0 = rbase + kh * 16 + 2 * tg;
+    const uint8_t* vr = tV + (kh * 16 + (mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
+#pragma unroll
+    for (int c = 0; c < 8; c += FP8 ? 2 : 1) {
+      uint32_t w[4];
+      ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vr + c * (FP8 ? 16 : 32));
+#pragma unroll
+      for (int i = 0; i < (FP8 ? 2 : 1); ++i) {
+        uint32_t b[4];   // keys 0-7 and 8-15 of even codes, then of odd ones (bf16: of 8 elements, then the next)
+        if constexpr (FP8) {
+          e4m3x4_to_f16x4(__byte_perm(w[2 * i], 0u, 0x3120), b[0], b[2]);
+          e4m3x4_to_f16x4(__byte_perm(w[2 * i + 1], 0u, 0x3120), b[1], b[3]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) b[h] = w[h];
+        }
+        if (EDGE) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int kb = k0 + (h & 1) * 8;
+            b[h] = clean_halves(keep_halves(b[h], kb <= top, kb + 1 <= top), FP8 ? 0x7c00u : 0x7f80u, bad);
+          }
+        }
+        const uint32_t a[4] = {b[0], b[2], b[1], b[3]};
+        if constexpr (FP8) mma_f16_16816(st.o[c + i], a, pb[0], pb[1]);
+        else mma_bf16_16816(st.o[c], a, pb[0], pb[1]);
+      }
+    }
+  }
+  if (EDGE && __any_sync(0xffffffffu, bad)) {
+    // rare: infinities and NaN of V reach the rows that see their key
+    for (int i = 0; i < KS; ++i) {
+      if (rbase + i > top) break;
+      const uint8_t* row = tV + (size_t)i * rb;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = 16 * c + (FP8 ? 2 * gq + (e >> 1) : 8 * (e >> 1) + gq);
+          float x;
+          if constexpr (FP8) x = (row[d] & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
+          else x = bf_lo(reinterpret_cast<const uint16_t*>(row)[d]);
+          if (!isfinite(x) && rbase + i <= lim[e & 1]) st.o[c][e] += x;
         }
     }
   }
@@ -850,11 +1034,15 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
       tok0 = s.begin + t0;
       ntok = min(pl.tb, min(s.len, a.max_q) - t0);
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) lim[hh] = min(s.pos0 + t0 + (gq + 8 * hh) / a.G, keys - 1);
+      for (int hh = 0; hh < 2; ++hh) lim[hh] = min(s.pos0 + t0 + (HALF ? 2 * tg + hh : gq + 8 * hh) / a.G, keys - 1);
     }
     const int low = SPARSE ? keys - 1 : keys - ntok;   // the least position a row of the block ends at
     state_init(st);
     load_q_rows<FP8>(qa, rowc, a, tok0, ntok, hs, active);
+    if constexpr (HALF) {   // the factors of rows 2 tg and 2 tg + 1
+      const float f0 = __shfl_sync(0xffffffffu, rowc[0], 8 * tg), f1 = __shfl_sync(0xffffffffu, rowc[0], 8 * tg + 4);
+      rowc[0] = f0, rowc[1] = f1;
+    }
     for (int t = tile; t < last; ++t) {
       const int s = (int)(fill % (uint32_t)pl.stages);
       if (!__all_sync(0xffffffffu,
@@ -867,10 +1055,14 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
         const uint8_t* tK = ring + (size_t)s * stage_bytes + (size_t)(rs * kRwKeys<FP8>) * rb;
         const uint8_t* tV = tK + (size_t)R * rb;
         const int tail = a.Hkv * kPgD + hs, off = hs * (FP8 ? kPgD : 2 * kPgD);
-        if (rbase + kRwKeys<FP8> - 1 > low)
-          row_step<FP8, true, HALF>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
-        else
-          row_step<FP8, false, HALF>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
+        const bool edge = rbase + kRwKeys<FP8> - 1 > low;
+        if constexpr (HALF) {
+          if (edge) row_step_few<FP8, true>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
+          else row_step_few<FP8, false>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
+        } else {
+          if (edge) row_step<FP8, true>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
+          else row_step<FP8, false>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
+        }
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&empty[s]);
@@ -883,12 +1075,27 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
       const long long base = (slot * a.Hkv + hs) * pl.RB;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
-        const int r = gq + 8 * hh;
+        const int r = HALF ? 2 * tg + hh : gq + 8 * hh;
+        float l = st.l[hh];
+        if constexpr (HALF) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        }
         if (r >= ntok * a.G) continue;
         float* po = part_o + (base + r) * kPgD;
-        if constexpr (FP8) {
-          // outputs go to the softmax's own reference m
-          const float f = st.mo[hh] == -INFINITY ? 0.f : exp2f(st.mo[hh] - st.m[hh] - kRwLift);
+        // codes: outputs go to the softmax's own reference m
+        const float f = !FP8 ? 1.f : st.mo[hh] == -INFINITY ? 0.f : exp2f(st.mo[hh] - st.m[hh] - kRwLift);
+        if constexpr (HALF) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if constexpr (FP8) {
+              *reinterpret_cast<float2*>(po + c * 16 + 2 * gq) = make_float2(st.o[c][hh] * f, st.o[c][2 + hh] * f);
+            } else {
+              po[c * 16 + gq] = st.o[c][hh];
+              po[c * 16 + 8 + gq] = st.o[c][2 + hh];
+            }
+          }
+        } else if constexpr (FP8) {
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<float4*>(po + c * 16 + 4 * tg) =
@@ -899,7 +1106,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
           for (int dt = 0; dt < 16; ++dt)
             *reinterpret_cast<float2*>(po + dt * 8 + 2 * tg) = make_float2(st.o[dt][2 * hh], st.o[dt][2 * hh + 1]);
         }
-        if (tg == 0) *reinterpret_cast<float2*>(part_ml + (base + r) * 2) = make_float2(st.m[hh], st.l[hh]);
+        if ((HALF ? gq : tg) == 0) *reinterpret_cast<float2*>(part_ml + (base + r) * 2) = make_float2(st.m[hh], l);
       }
     }
   }
