@@ -11,14 +11,13 @@
 //
 // Few-row attention: softmax(scale q.K^T) V by one pass with a running
 // maximum and sum.  It reads the cache once, 2 * row bytes per position for
-// 4 * 128 * Hq flops, so it is bound by HBM; the row side of the matrix
-// instructions (mma.sync, 16 rows) holds the G query heads of the chunk's
-// tokens, which share the kv head's rows; with 8 rows at most the keys take
-// that side.
+// 4 * 128 * Hq flops, so it is bound by HBM; the 16-row side of the matrix
+// instructions (mma.sync, 16 x 8) takes the cache's, the 8-column side the G
+// query heads of the chunk's tokens, which share the kv head's rows.
 //
 //   paged_write_kernel       one warp per token (K and V)
 //   paged_gather_kernel      one warp per selected row (K and V)
-//   paged_attn_rows_kernel   units of (16-row block of queries, tile of
+//   paged_attn_rows_kernel   units of (block of up to 24 query rows, tile of
 //       positions, all kv heads), flattened over the batch and cut evenly
 //       over one CTA per SM; partials of (max, sum, output)
 //   paged_attn_rows_merge_kernel   folds them by the log-sum-exp rule
@@ -250,6 +249,11 @@ constexpr int kRwConsumers = 8;
 // 8 x 32K E4M3 positions, 115 with).
 constexpr int kRwThreads = (kRwConsumers + 4) * 32, kRwConsumerRegs = 224, kRwOtherRegs = 56;
 constexpr int kRwMaxStages = 8;
+// Query rows of a block, in eights: what the consumers' registers hold (drafts
+// of 20 rows, 16 sequences, 8 kv heads: bf16 82 us in blocks of 16, 68 of 24;
+// E4M3 65 and 78, as 24 rows spill beside two scales and references).
+template <bool FP8>
+constexpr int kRwRows = FP8 ? 16 : 24;
 constexpr int kRwBarBytes = 256;       // mbarriers, abort word, plan, scan
 static_assert((2 * kRwMaxStages + 2 + kRwThreads / 32) * 8 <= kRwBarBytes, "barrier block");
 constexpr int kRwStageBytes = 222 * 1024;
@@ -337,28 +341,29 @@ __device__ __forceinline__ long long floor_div(long long x, long long d) {
   return (unsigned long long)(x | d) >> 32 ? x / d : (long long)((unsigned)x / (unsigned)d);
 }
 
-// Query fragments (the M side): row r of the block is token t0 + r / G, head
-// r % G of kv head g.  For bf16 keys the usual layout; for codes, fp16 with
-// the reduction index permuted to what one ldmatrix of 16 codes gives (lane t
-// holds elements 4t .. 4t+3 of every 16), each row scaled by a power of two
-// that brings its largest magnitude to [2^14, 2^15): exact for every element
-// within 2^-31 of the largest, and undone in fp32 (`rowc`).
-template <bool FP8>
-__device__ __forceinline__ void load_q_rows(uint32_t (&qa)[8][4], float (&rowc)[2], const PagedArgs& a, int tok0,
+// Query fragments (the 8-column side): row 8 n + gq of the block is token
+// tok0 + row / G, head row % G of kv head g.  For bf16 keys the usual layout;
+// for codes, fp16 with the reduction index permuted to what one ldmatrix of 16
+// codes gives (lane t holds elements 4t .. 4t+3 of every 16), each row scaled
+// by a power of two that brings its largest magnitude to [2^14, 2^15): exact
+// for every element within 2^-31 of the largest, and undone in fp32 (`rowc`,
+// for rows 8 n + 2 tg + {0, 1}).
+template <bool FP8, int NB>
+__device__ __forceinline__ void load_q_rows(uint32_t (&q)[NB][8][2], float (&rowc)[NB][2], const PagedArgs& a, int tok0,
                                             int ntok, int g, bool active) {
   const int lane = threadIdx.x & 31, gq = lane >> 2, tg = lane & 3;
 #pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
-    const int r = gq + 8 * hh;
+  for (int nb = 0; nb < NB; ++nb) {
+    const int r = gq + 8 * nb;
     const bool on = active && r < ntok * a.G;
     const uint16_t* src = a.q + (long long)(tok0 + (on ? r / a.G : 0)) * a.q_stride +
                           ((active ? g : 0) * a.G + (on ? r % a.G : 0)) * kPgD;
-    rowc[hh] = a.qscale;
+    float f = a.qscale;
     if constexpr (!FP8) {
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        qa[kk][hh] = on ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * tg)) : 0u;
-        qa[kk][2 + hh] = on ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + 2 * tg)) : 0u;
+        q[nb][kk][0] = on ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * tg)) : 0u;
+        q[nb][kk][1] = on ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + 2 * tg)) : 0u;
       }
     } else {
       uint2 v[8];
@@ -378,13 +383,15 @@ __device__ __forceinline__ void load_q_rows(uint32_t (&qa)[8][4], float (&rowc)[
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
       const int e = min(max((int)(am >> 7) - 141, -100), 113);   // largest * 2^-e in [2^14, 2^15)
       const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-      rowc[hh] = a.qscale * __uint_as_float((uint32_t)(127 + e) << 23);
+      f *= __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        qa[kk][hh] = pack_f16x2(bf_lo(v[kk].x) * inv, bf_hi(v[kk].x) * inv);
-        qa[kk][2 + hh] = pack_f16x2(bf_lo(v[kk].y) * inv, bf_hi(v[kk].y) * inv);
+        q[nb][kk][0] = pack_f16x2(bf_lo(v[kk].x) * inv, bf_hi(v[kk].x) * inv);
+        q[nb][kk][1] = pack_f16x2(bf_lo(v[kk].y) * inv, bf_hi(v[kk].y) * inv);
       }
     }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) rowc[nb][e] = __shfl_sync(0xffffffffu, f, 8 * tg + 4 * e);
   }
 }
 
@@ -397,22 +404,29 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Running state of one warp's 16 rows: output, its reference (base-2
+// Running state of one warp's 8 NB rows: output, its reference (base-2
 // logarithm), the softmax's reference and sum.  For codes the output's
 // reference mo bounds z + log2(scale of v), so the weights that multiply the
-// codes stay within fp16; for bf16 one reference serves both.
+// codes stay within fp16; for bf16 one reference serves both.  A lane holds
+// rows 8 n + 2 tg + {0, 1}; o[n][c][e]: row 8 n + 2 tg + (e & 1), element
+// 16 c + 2 gq + (e >> 1) (codes) or 16 c + 8 (e >> 1) + gq.
+template <int NB>
 struct RowState {
-  float o[16][4];
-  float m[2], l[2], mo[2];
+  float o[NB][8][4];
+  float m[NB][2], l[NB][2], mo[NB][2];   // l: this lane's part of the sum
 };
 
-__device__ __forceinline__ void state_init(RowState& st) {
+template <int NB>
+__device__ __forceinline__ void state_init(RowState<NB>& st) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) st.o[i][e] = 0.f;
-  st.m[0] = st.m[1] = st.mo[0] = st.mo[1] = -INFINITY;
-  st.l[0] = st.l[1] = 0.f;
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.o[nb][i][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) st.m[nb][e] = st.mo[nb][e] = -INFINITY, st.l[nb][e] = 0.f;
+  }
 }
 
 // Zeroes the halves of a pair of 16-bit values whose bit in `keep` is clear.
@@ -431,211 +445,6 @@ __device__ __forceinline__ uint32_t clean_halves(uint32_t v, uint32_t ex, bool& 
 // = 2^15 and keep what is within 2^-33 of the largest weight of their row.
 constexpr float kRwLift = 9.f, kRwLazy = 6.f;
 
-// One step over a slice of a tile (KS positions): scores, running maximum and
-// sum, output.  tK, tV: the slice's first row, this kv head; rb: bytes from
-// row to row; sK, sV: the scale bytes of this head in the slice's first row.
-// Key rbase + i is seen by row r when it is <= lim[r] (-1: never).
-// EDGE: some key of the slice is not seen by some row.  Then V rows that no
-// row sees are zeroed, and infinities and NaN in V are taken out of the
-// product and added to the rows that see them only.
-template <bool FP8, bool EDGE>
-__device__ __forceinline__ void row_step(RowState& st, const uint32_t (&qa)[8][4], const float (&rowc)[2],
-                                         const uint8_t* tK, const uint8_t* tV, int rb, const uint8_t* sK,
-                                         const uint8_t* sV, int rbase, const int (&lim)[2], int top) {
-  constexpr int KS = kRwKeys<FP8>, NT = KS / 8, NH = 2, NE = 4;
-  const int lane = threadIdx.x & 31, tg = lane & 3, mtx = lane >> 3;
-  float sc[NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
-  float kscale[NT][2], vexp[NT][2];
-  if constexpr (FP8) {
-    const uint8_t* kr = tK + ((mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
-#pragma unroll
-    for (int c = 0; c < 8; c += 2) {
-#pragma unroll
-      for (int kh = 0; kh < KS / 16; ++kh) {   // 16 keys x 32 codes
-        uint32_t w[4];                         // keys 0-7 and 8-15 of chunk c, then of chunk c + 1
-        ldmatrix_x4(w[0], w[1], w[2], w[3], kr + kh * 16 * rb + c * 16);
-        uint32_t b[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], b[i][0], b[i][1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mma_f16_16816(sc[2 * kh + (i & 1)], qa[c + (i >> 1)], b[i][0], b[i][1]);
-      }
-    }
-    // lane l converts the scales of key l; each lane takes those of its keys
-    const float ks = e8m0_value(sK[lane * rb]), ve = e8m0_exponent(sV[lane * rb]);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        kscale[nt][e] = __shfl_sync(0xffffffffu, ks, nt * 8 + tg * 2 + e);
-        vexp[nt][e] = __shfl_sync(0xffffffffu, ve, nt * 8 + tg * 2 + e);
-      }
-  } else {
-    float sd[2][4];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sd[nt][e] = 0.f;
-    const uint8_t* kr = tK + ((mtx >> 1) * 8 + (lane & 7)) * rb + (mtx & 1) * 16;
-#pragma unroll
-    for (int kk = 0; kk < 8; kk += 2) {
-      uint32_t b0, b1, b2, b3, c0, c1, c2, c3;
-      ldmatrix_x4(b0, b1, b2, b3, kr + kk * 32);
-      ldmatrix_x4(c0, c1, c2, c3, kr + kk * 32 + 32);
-      mma_bf16_16816(sc[0], qa[kk], b0, b1);
-      mma_bf16_16816(sc[1], qa[kk], b2, b3);
-      mma_bf16_16816(sd[0], qa[kk + 1], c0, c1);
-      mma_bf16_16816(sd[1], qa[kk + 1], c2, c3);
-    }
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][e] += sd[nt][e];
-  }
-  // base-2 logits; masked ones are -inf whatever the product was
-  float mx[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const int hh = e >> 1;
-      float z = sc[nt][e] * rowc[hh];
-      if constexpr (FP8) z *= kscale[nt][e & 1];
-      if (EDGE) z = rbase + nt * 8 + tg * 2 + (e & 1) <= lim[hh] ? z : -INFINITY;
-      sc[nt][e] = z;
-      mx[hh] = fmaxf(mx[hh], z);
-      // (an exponent that is NaN makes the weight NaN, not the reference)
-      if constexpr (FP8) mv[hh] = fmaxf(mv[hh], z + vexp[nt][e & 1]);
-    }
-  float alpha[2] = {1.f, 1.f}, muse[2];
-#pragma unroll
-  for (int hh = 0; hh < NH; ++hh) {
-    float v = mx[hh];
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-    const float mnew = v > st.m[hh] + kRwLazy ? v : st.m[hh];
-    muse[hh] = mnew == -INFINITY ? 0.f : mnew;
-    alpha[hh] = mnew == st.m[hh] ? 1.f : ex2(st.m[hh] - muse[hh]);
-    st.m[hh] = mnew;
-  }
-  float rsum[2] = {0.f, 0.f};
-  float wt[NT][4] = {};   // the weights that multiply V
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      wt[nt][e] = ex2(sc[nt][e] - muse[e >> 1]);
-      rsum[e >> 1] += wt[nt][e];
-    }
-#pragma unroll
-  for (int hh = 0; hh < NH; ++hh) {
-    float v = rsum[hh];
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    v += __shfl_xor_sync(0xffffffffu, v, 2);
-    st.l[hh] = st.l[hh] * alpha[hh] + v;
-  }
-  if constexpr (FP8) {   // the output's own reference and weights
-#pragma unroll
-    for (int hh = 0; hh < NH; ++hh) {
-      float v = mv[hh];
-      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-      const float mnew = v > st.mo[hh] + kRwLazy ? v : st.mo[hh];
-      const float mu = mnew == -INFINITY ? 0.f : mnew;
-      alpha[hh] = mnew == st.mo[hh] ? 1.f : ex2(st.mo[hh] - mu);
-      st.mo[hh] = mnew;
-      mv[hh] = mu - kRwLift;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        float zo = sc[nt][e] + vexp[nt][e & 1];
-        if (EDGE) zo = sc[nt][e] == -INFINITY ? -INFINITY : zo;   // (a masked row's scale may be NaN)
-        wt[nt][e] = ex2(zo - mv[e >> 1]);
-      }
-  }
-  if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {   // a reference moved
-#pragma unroll
-    for (int dt = 0; dt < 16; ++dt) {
-      st.o[dt][0] *= alpha[0];
-      st.o[dt][1] *= alpha[0];
-      st.o[dt][2] *= alpha[1];
-      st.o[dt][3] *= alpha[1];
-    }
-  }
-  bool bad = false;
-#pragma unroll
-  for (int kh = 0; kh < KS / 16; ++kh) {
-    // V fragment registers hold keys 2 tg, 2 tg + 1 (b0) and those + 8 (b1)
-    const int k0 = rbase + kh * 16 + 2 * tg;
-    const uint8_t* vr = tV + (kh * 16 + (mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
-    const float(&u)[4] = wt[2 * kh], (&v)[4] = wt[2 * kh + 1];
-    if constexpr (FP8) {
-      uint32_t pa[4] = {pack_f16x2(u[0], u[1]), pack_f16x2(u[2], u[3]), pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
-#pragma unroll
-      for (int c = 0; c < 8; c += 2) {
-        uint32_t w[4];   // transposed: keys 2 tg, 2 tg + 1 x codes 2 gq, 2 gq + 1 of a chunk
-        ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vr + c * 16);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t b[4];   // even codes of keys 0-7 and 8-15, then odd ones
-          e4m3x4_to_f16x4(__byte_perm(w[2 * i], 0u, 0x3120), b[0], b[2]);
-          e4m3x4_to_f16x4(__byte_perm(w[2 * i + 1], 0u, 0x3120), b[1], b[3]);
-          if (EDGE) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const int kb = k0 + (h & 1) * 8;
-              b[h] = clean_halves(keep_halves(b[h], kb <= top, kb + 1 <= top), 0x7c00u, bad);
-            }
-          }
-          mma_f16_16816(st.o[2 * (c + i)], pa, b[0], b[1]);
-          mma_f16_16816(st.o[2 * (c + i) + 1], pa, b[2], b[3]);
-        }
-      }
-    } else {
-      uint32_t pa[4] = {pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]),
-                        pack_bf16x2(v[2], v[3])};
-#pragma unroll
-      for (int dt = 0; dt < 16; dt += 2) {
-        uint32_t b[4];
-        ldmatrix_x4_trans(b[0], b[1], b[2], b[3], vr + dt * 16);
-        if (EDGE) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int kb = k0 + (h & 1) * 8;
-            b[h] = clean_halves(keep_halves(b[h], kb <= top, kb + 1 <= top), 0x7f80u, bad);
-          }
-        }
-        mma_bf16_16816(st.o[dt], pa, b[0], b[1]);
-        mma_bf16_16816(st.o[dt + 1], pa, b[2], b[3]);
-      }
-    }
-  }
-  if (EDGE && __any_sync(0xffffffffu, bad)) {
-    // rare: infinities and NaN of V reach the rows that see their key
-    for (int i = 0; i < KS; ++i) {
-      if (rbase + i > top) break;
-      const uint8_t* row = tV + (size_t)i * rb;
-#pragma unroll
-      for (int dt = 0; dt < 16; ++dt)
-#pragma unroll
-        for (int e = 0; e < NE; ++e) {
-          // column of st.o[dt][e]: see the partials' stores
-          const int d = FP8 ? (dt >> 1) * 16 + 4 * tg + 2 * (e & 1) + (dt & 1) : dt * 8 + 2 * tg + (e & 1);
-          float x;
-          if constexpr (FP8) x = (row[d] & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
-          else x = bf_lo(reinterpret_cast<const uint16_t*>(row)[d]);
-          if (!isfinite(x) && rbase + i <= lim[e >> 1]) st.o[dt][e] += x;
-        }
-    }
-  }
-}
-
 // An 8 x 8 block of 16-bit values, transposed across the warp.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   uint32_t r;
@@ -643,26 +452,34 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   return r;
 }
 
-// row_step for blocks of at most 8 rows, with the keys (then the output's
-// elements) on the 16-row side of the products and the query rows on the
-// 8-column side: half as many products as with 8 of 16 rows empty (E4M3, one
-// token of each of 8 x 32K positions 95 us for 97, of 8 x 2048 selected ones
-// 14.4 for 15.4).  A lane holds
-// rows 2 tg + {0, 1} and, of every 16 keys, gq and gq + 8; its parts of a
-// row's sum are added up at the end, and no lane needs another's maximum
-// until a reference rises.  st.o[c][e]: row 2 tg + (e & 1), element
-// 16 c + 2 gq + (e >> 1) (codes) or 16 c + 8 (e >> 1) + gq.
-template <bool FP8, bool EDGE>
-__device__ __forceinline__ void row_step_few(RowState& st, const uint32_t (&qa)[8][4], const float (&rowc)[2],
-                                             const uint8_t* tK, const uint8_t* tV, int rb, const uint8_t* sK,
-                                             const uint8_t* sV, int rbase, const int (&lim)[2], int top) {
+// One step over a slice of a tile (KS positions): scores, running maximum and
+// sum, output.  The keys, then the output's elements, are on the 16-row side
+// of the products and the query rows on the 8-column side, so a converted key
+// or value serves all NB blocks of 8 rows and few rows leave no product empty
+// (E4M3, rows on the 16-row side: one token of each of 8 x 32K positions 97 us
+// for 95, of 8 x 2048 selected ones 15.4 for 14.4).  No lane needs another's
+// maximum until a reference rises.
+// tK, tV: the slice's first row, this kv head; rb: bytes from row to row; sK,
+// sV: the scale bytes of this head in the slice's first row.  Key rbase + i is
+// seen by row r when it is <= lim[r] (-1: never).
+// EDGE: some key of the slice is not seen by some row.  Then V rows that no
+// row sees are zeroed, and infinities and NaN in V are taken out of the
+// product and added to the rows that see them only.
+template <bool FP8, bool EDGE, int NB>
+__device__ __forceinline__ void row_step(RowState<NB>& st, const uint32_t (&q)[NB][8][2], const float (&rowc)[NB][2],
+                                         const uint8_t* tK, const uint8_t* tV, int rb, const uint8_t* sK,
+                                         const uint8_t* sV, int rbase, const int (&lim)[NB][2], int top) {
   constexpr int KS = kRwKeys<FP8>, KH = KS / 16;
   const int lane = threadIdx.x & 31, gq = lane >> 2, tg = lane & 3, mtx = lane >> 3;
-  float sc[KH][4], sd[KH][4];
+  float sc[NB][KH][4], sd[KH][4];   // (one block: two sums a score, for products in flight)
 #pragma unroll
   for (int kh = 0; kh < KH; ++kh)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sc[kh][e] = sd[kh][e] = 0.f;
+    for (int e = 0; e < 4; ++e) {
+      sd[kh][e] = 0.f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) sc[nb][kh][e] = 0.f;
+    }
   const uint8_t* kr = tK + ((mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
   float kscale[KH][2], vexp[KH][2];
   if constexpr (FP8) {
@@ -675,8 +492,11 @@ __device__ __forceinline__ void row_step_few(RowState& st, const uint32_t (&qa)[
         uint32_t a[2][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], a[i >> 1][i & 1], a[i >> 1][2 + (i & 1)]);
-        mma_f16_16816(sc[kh], a[0], qa[c][0], qa[c][2]);
-        mma_f16_16816(sd[kh], a[1], qa[c + 1][0], qa[c + 1][2]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma_f16_16816(sc[nb][kh], a[0], q[nb][c][0], q[nb][c][1]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          mma_f16_16816(NB == 1 ? sd[kh] : sc[nb][kh], a[1], q[nb][c + 1][0], q[nb][c + 1][1]);
       }
     // lane l converts the scales of key l; each lane takes those of its keys
     const float ks = e8m0_value(sK[lane * rb]), ve = e8m0_exponent(sV[lane * rb]);
@@ -693,86 +513,102 @@ __device__ __forceinline__ void row_step_few(RowState& st, const uint32_t (&qa)[
       uint32_t a[4], b[4];   // keys 0-7 and 8-15, first and last 8 of 16 elements
       ldmatrix_x4(a[0], a[1], a[2], a[3], kr + kk * 32);
       ldmatrix_x4(b[0], b[1], b[2], b[3], kr + kk * 32 + 32);
-      mma_bf16_16816(sc[0], a, qa[kk][0], qa[kk][2]);
-      mma_bf16_16816(sd[0], b, qa[kk + 1][0], qa[kk + 1][2]);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(sc[nb][0], a, q[nb][kk][0], q[nb][kk][1]);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        mma_bf16_16816(NB == 1 ? sd[0] : sc[nb][0], b, q[nb][kk + 1][0], q[nb][kk + 1][1]);
     }
   }
   // base-2 logits; masked ones are -inf whatever the product was
-  float mx[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-  for (int kh = 0; kh < KH; ++kh)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = e & 1, h = e >> 1;
-      float z = (sc[kh][e] + sd[kh][e]) * rowc[row];
-      if constexpr (FP8) z *= kscale[kh][h];
-      if (EDGE) z = rbase + kh * 16 + h * 8 + gq <= lim[row] ? z : -INFINITY;
-      sc[kh][e] = z;
-      mx[row] = fmaxf(mx[row], z);
-      // (an exponent that is NaN makes the weight NaN, not the reference)
-      if constexpr (FP8) mv[row] = fmaxf(mv[row], z + vexp[kh][h]);
-    }
+  float mx[NB][2], mv[NB][2];
   bool up = false;
 #pragma unroll
-  for (int row = 0; row < 2; ++row) {
-    up |= mx[row] > st.m[row] + kRwLazy;
-    if constexpr (FP8) up |= mv[row] > st.mo[row] + kRwLazy;
-  }
-  if (__any_sync(0xffffffffu, up)) {   // a reference rises
-    float alpha[2];
+  for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+    for (int row = 0; row < 2; ++row) mx[nb][row] = mv[nb][row] = -INFINITY;
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = e & 1, h = e >> 1;
+        float z = (NB == 1 ? sc[nb][kh][e] + sd[kh][e] : sc[nb][kh][e]) * rowc[nb][row];
+        if constexpr (FP8) z *= kscale[kh][h];
+        if (EDGE) z = rbase + kh * 16 + h * 8 + gq <= lim[nb][row] ? z : -INFINITY;
+        sc[nb][kh][e] = z;
+        mx[nb][row] = fmaxf(mx[nb][row], z);
+        // (an exponent that is NaN makes the weight NaN, not the reference)
+        if constexpr (FP8) mv[nb][row] = fmaxf(mv[nb][row], z + vexp[kh][h]);
+      }
 #pragma unroll
     for (int row = 0; row < 2; ++row) {
-      alpha[row] = 1.f;
-      float v = mx[row], u = mv[row];
+      up |= mx[nb][row] > st.m[nb][row] + kRwLazy;
+      if constexpr (FP8) up |= mv[nb][row] > st.mo[nb][row] + kRwLazy;
+    }
+  }
+  if (__any_sync(0xffffffffu, up)) {   // a reference rises
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-        if constexpr (FP8) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
-      }
-      if (v > st.m[row] + kRwLazy) {
-        alpha[row] = ex2(st.m[row] - v);
-        st.m[row] = v;
-        st.l[row] *= alpha[row];
-      }
-      if constexpr (FP8) {   // the output's own reference
+    for (int nb = 0; nb < NB; ++nb) {
+      float alpha[2];
+#pragma unroll
+      for (int row = 0; row < 2; ++row) {
         alpha[row] = 1.f;
-        if (u > st.mo[row] + kRwLazy) {
-          alpha[row] = ex2(st.mo[row] - u);
-          st.mo[row] = u;
+        float v = mx[nb][row], u = mv[nb][row];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+          if constexpr (FP8) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+        }
+        if (v > st.m[nb][row] + kRwLazy) {
+          alpha[row] = ex2(st.m[nb][row] - v);
+          st.m[nb][row] = v;
+          st.l[nb][row] *= alpha[row];
+        }
+        if constexpr (FP8) {   // the output's own reference
+          alpha[row] = 1.f;
+          if (u > st.mo[nb][row] + kRwLazy) {
+            alpha[row] = ex2(st.mo[nb][row] - u);
+            st.mo[nb][row] = u;
+          }
         }
       }
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[nb][c][e] *= alpha[e & 1];
+    }
+  }
+  uint32_t pb[NB][KH][2];   // weights of 8 keys x 8 rows, as the products want them
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    float mu[2], mo[2];
+#pragma unroll
+    for (int row = 0; row < 2; ++row) {
+      mu[row] = st.m[nb][row] == -INFINITY ? 0.f : st.m[nb][row];
+      mo[row] = (st.mo[nb][row] == -INFINITY ? 0.f : st.mo[nb][row]) - kRwLift;
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
+    for (int kh = 0; kh < KH; ++kh)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) st.o[c][e] *= alpha[e & 1];
-  }
-  float mu[2], mo[2];
+      for (int h = 0; h < 2; ++h) {
+        float wt[2];
 #pragma unroll
-  for (int row = 0; row < 2; ++row) {
-    mu[row] = st.m[row] == -INFINITY ? 0.f : st.m[row];
-    mo[row] = (st.mo[row] == -INFINITY ? 0.f : st.mo[row]) - kRwLift;
+        for (int row = 0; row < 2; ++row) {
+          const float z = sc[nb][kh][2 * h + row];
+          wt[row] = ex2(z - mu[row]);
+          st.l[nb][row] += wt[row];
+          if constexpr (FP8) {
+            float zo = z + vexp[kh][h];
+            if (EDGE) zo = z == -INFINITY ? -INFINITY : zo;   // (a masked row's scale may be NaN)
+            wt[row] = ex2(zo - mo[row]);
+          }
+        }
+        pb[nb][kh][h] = transpose_8x8(FP8 ? pack_f16x2(wt[0], wt[1]) : pack_bf16x2(wt[0], wt[1]));
+      }
   }
   bool bad = false;
 #pragma unroll
   for (int kh = 0; kh < KH; ++kh) {
-    uint32_t pb[2];   // weights of 8 keys x 8 rows, then as the products want them
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float wt[2];
-#pragma unroll
-      for (int row = 0; row < 2; ++row) {
-        const float z = sc[kh][2 * h + row];
-        wt[row] = ex2(z - mu[row]);
-        st.l[row] += wt[row];
-        if constexpr (FP8) {
-          float zo = z + vexp[kh][h];
-          if (EDGE) zo = z == -INFINITY ? -INFINITY : zo;   // (a masked row's scale may be NaN)
-          wt[row] = ex2(zo - mo[row]);
-        }
-      }
-      pb[h] = transpose_8x8(FP8 ? pack_f16x2(wt[0], wt[1]) : pack_bf16x2(wt[0], wt[1]));
-    }
     // V fragment registers hold keys 2 tg, 2 tg + 1 and those + 8
     const int k0 = rbase + kh * 16 + 2 * tg;
     const uint8_t* vr = tV + (kh * 16 + (mtx & 1) * 8 + (lane & 7)) * rb + (mtx >> 1) * 16;
@@ -798,8 +634,11 @@ __device__ __forceinline__ void row_step_few(RowState& st, const uint32_t (&qa)[
           }
         }
         const uint32_t a[4] = {b[0], b[2], b[1], b[3]};
-        if constexpr (FP8) mma_f16_16816(st.o[c + i], a, pb[0], pb[1]);
-        else mma_bf16_16816(st.o[c], a, pb[0], pb[1]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if constexpr (FP8) mma_f16_16816(st.o[nb][c + i], a, pb[nb][kh][0], pb[nb][kh][1]);
+          else mma_bf16_16816(st.o[nb][c], a, pb[nb][kh][0], pb[nb][kh][1]);
+        }
       }
     }
   }
@@ -816,13 +655,15 @@ __device__ __forceinline__ void row_step_few(RowState& st, const uint32_t (&qa)[
           float x;
           if constexpr (FP8) x = (row[d] & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
           else x = bf_lo(reinterpret_cast<const uint16_t*>(row)[d]);
-          if (!isfinite(x) && rbase + i <= lim[e & 1]) st.o[c][e] += x;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            if (!isfinite(x) && rbase + i <= lim[nb][e & 1]) st.o[nb][c][e] += x;
         }
     }
   }
 }
 
-template <bool FP8, bool SPARSE, bool HALF>
+template <bool FP8, bool SPARSE, int NB>
 __global__ void __launch_bounds__(kRwThreads, 1)
 paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__ part_o, float* __restrict__ part_ml,
                        int* __restrict__ err) {
@@ -1014,9 +855,9 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
   const int gq = lane >> 2, tg = lane & 3;
   const int hs = warp / pl.wph, rs = warp % pl.wph;
   const bool active = hs < a.Hkv;
-  RowState st;
-  uint32_t qa[8][4];
-  float rowc[2];
+  RowState<NB> st;
+  uint32_t qa[NB][8][2];
+  float rowc[NB][2];
   uint32_t fill = 0;
   bool ok = true;
   for (; left > 0 && ok; ++p, tile = 0) {
@@ -1025,24 +866,22 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
     const int last = (int)min((long long)tiles, tile + left);
     if (tile >= last) continue;
     left -= last - tile;
-    int tok0 = p, ntok = 1, lim[2];
+    int tok0 = p, ntok = 1, lim[NB][2];
     if constexpr (SPARSE) {
-      lim[0] = lim[1] = keys - 1;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) lim[nb][0] = lim[nb][1] = keys - 1;
     } else {
       const int b = p / pl.nrb, t0 = p % pl.nrb * pl.tb;
       const SeqSpan s = seq_span(a.q_start, a.kv_len, b, a.N, capacity);
       tok0 = s.begin + t0;
       ntok = min(pl.tb, min(s.len, a.max_q) - t0);
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) lim[hh] = min(s.pos0 + t0 + (HALF ? 2 * tg + hh : gq + 8 * hh) / a.G, keys - 1);
+      for (int r = 0; r < 2 * NB; ++r)
+        lim[r >> 1][r & 1] = min(s.pos0 + t0 + (8 * (r >> 1) + 2 * tg + (r & 1)) / a.G, keys - 1);
     }
     const int low = SPARSE ? keys - 1 : keys - ntok;   // the least position a row of the block ends at
     state_init(st);
-    load_q_rows<FP8>(qa, rowc, a, tok0, ntok, hs, active);
-    if constexpr (HALF) {   // the factors of rows 2 tg and 2 tg + 1
-      const float f0 = __shfl_sync(0xffffffffu, rowc[0], 8 * tg), f1 = __shfl_sync(0xffffffffu, rowc[0], 8 * tg + 4);
-      rowc[0] = f0, rowc[1] = f1;
-    }
+    load_q_rows<FP8, NB>(qa, rowc, a, tok0, ntok, hs, active);
     for (int t = tile; t < last; ++t) {
       const int s = (int)(fill % (uint32_t)pl.stages);
       if (!__all_sync(0xffffffffu,
@@ -1055,14 +894,10 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
         const uint8_t* tK = ring + (size_t)s * stage_bytes + (size_t)(rs * kRwKeys<FP8>) * rb;
         const uint8_t* tV = tK + (size_t)R * rb;
         const int tail = a.Hkv * kPgD + hs, off = hs * (FP8 ? kPgD : 2 * kPgD);
-        const bool edge = rbase + kRwKeys<FP8> - 1 > low;
-        if constexpr (HALF) {
-          if (edge) row_step_few<FP8, true>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
-          else row_step_few<FP8, false>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
-        } else {
-          if (edge) row_step<FP8, true>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
-          else row_step<FP8, false>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
-        }
+        if (rbase + kRwKeys<FP8> - 1 > low)
+          row_step<FP8, true, NB>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
+        else
+          row_step<FP8, false, NB>(st, qa, rowc, tK + off, tV + off, rb, tK + tail, tV + tail, rbase, lim, keys - 1);
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&empty[s]);
@@ -1074,40 +909,31 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
       const long long slot = ((long long)p + blockIdx.x) * pl.wph + rs;
       const long long base = (slot * a.Hkv + hs) * pl.RB;
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int r = HALF ? 2 * tg + hh : gq + 8 * hh;
-        float l = st.l[hh];
-        if constexpr (HALF) {
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * nb + 2 * tg + e;
+          float l = st.l[nb][e];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        }
-        if (r >= ntok * a.G) continue;
-        float* po = part_o + (base + r) * kPgD;
-        // codes: outputs go to the softmax's own reference m
-        const float f = !FP8 ? 1.f : st.mo[hh] == -INFINITY ? 0.f : exp2f(st.mo[hh] - st.m[hh] - kRwLift);
-        if constexpr (HALF) {
+          if (r >= ntok * a.G) continue;
+          float* po = part_o + (base + r) * kPgD;
+          if constexpr (FP8) {
+            // outputs go to the softmax's own reference m
+            const float f = st.mo[nb][e] == -INFINITY ? 0.f : exp2f(st.mo[nb][e] - st.m[nb][e] - kRwLift);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if constexpr (FP8) {
-              *reinterpret_cast<float2*>(po + c * 16 + 2 * gq) = make_float2(st.o[c][hh] * f, st.o[c][2 + hh] * f);
-            } else {
-              po[c * 16 + gq] = st.o[c][hh];
-              po[c * 16 + 8 + gq] = st.o[c][2 + hh];
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<float2*>(po + c * 16 + 2 * gq) =
+                  make_float2(st.o[nb][c][e] * f, st.o[nb][c][2 + e] * f);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              po[c * 16 + gq] = st.o[nb][c][e];
+              po[c * 16 + 8 + gq] = st.o[nb][c][2 + e];
             }
           }
-        } else if constexpr (FP8) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<float4*>(po + c * 16 + 4 * tg) =
-                make_float4(st.o[2 * c][2 * hh] * f, st.o[2 * c + 1][2 * hh] * f, st.o[2 * c][2 * hh + 1] * f,
-                            st.o[2 * c + 1][2 * hh + 1] * f);
-        } else {
-#pragma unroll
-          for (int dt = 0; dt < 16; ++dt)
-            *reinterpret_cast<float2*>(po + dt * 8 + 2 * tg) = make_float2(st.o[dt][2 * hh], st.o[dt][2 * hh + 1]);
+          if (gq == 0) *reinterpret_cast<float2*>(part_ml + (base + r) * 2) = make_float2(st.m[nb][e], l);
         }
-        if ((HALF ? gq : tg) == 0) *reinterpret_cast<float2*>(part_ml + (base + r) * 2) = make_float2(st.m[hh], l);
-      }
     }
   }
 }
@@ -1322,8 +1148,9 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
 
 RowsPlan rows_plan(int fp8, int B, int Hkv, int G, int max_q) {
   RowsPlan pl;
-  pl.tb = 16 / G < max_q ? 16 / G : max_q;
-  pl.nrb = (max_q + pl.tb - 1) / pl.tb;
+  const int most = (fp8 ? kRwRows<true> : kRwRows<false>) / G;
+  pl.nrb = (max_q + most - 1) / most;
+  pl.tb = (max_q + pl.nrb - 1) / pl.nrb;
   pl.RB = pl.tb * G;
   pl.P = B * pl.nrb;
   pl.wph = kRwConsumers / Hkv;   // 8, 4, 2 or 1 for Hkv <= 8: tiles and pages are powers of two, neither
@@ -1350,7 +1177,9 @@ cudaError_t launch_rows(const PagedArgs& a, void* parts, int* err, cudaStream_t 
   float* po = reinterpret_cast<float*>(p);
   float* pml = reinterpret_cast<float*>(p + align256p(slots * kPgD * 4));
   const size_t smem = kRwBarBytes + (size_t)pl.stages * 2 * pl.R * pl.row_bytes;
-  auto kern = pl.RB <= 8 ? paged_attn_rows_kernel<FP8, SPARSE, true> : paged_attn_rows_kernel<FP8, SPARSE, false>;
+  auto kern = pl.RB <= 8    ? paged_attn_rows_kernel<FP8, SPARSE, 1>
+              : pl.RB <= 16 ? paged_attn_rows_kernel<FP8, SPARSE, 2>
+                            : paged_attn_rows_kernel<FP8, SPARSE, FP8 || SPARSE ? 2 : 3>;   // (one token: 16 rows at most)
   cudaError_t e = ensure_dynamic_smem((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((unsigned)pl.W), dim3(kRwThreads), smem, st, a, pl, po, pml, err);
@@ -1421,15 +1250,15 @@ cudaError_t launch_paged_rows(const PagedArgs& a, int fp8, void* ws, cudaStream_
 }
 
 // Chunks of few query rows per kv head go to the row kernel, which reads the
-// cache once per 16 rows; longer ones to the tensor cores, which read it once
+// cache once per 16 or 24 rows; longer ones to the tensor cores, which read it once
 // per 256.  Measured, us (row kernel / tensor cores; all of the batch alike):
 //   E4M3, 8 kv heads x 4:  20 rows, 4 x 16K positions   76 / 209
 //                          64 rows, 4 x 16K             133 / 209
 //                          128 rows, 1 x 4K             37 / 55;  256 rows 55 / 53
-//   bf16, 8 kv heads x 4:  20 rows, 4 x 16K             111 / 127
-//                          32 rows, 4 x 16K             115 / 127;  64 rows 197 / 131
+//   bf16, 8 kv heads x 4:  20 rows, 4 x 16K             74 / 127
+//                          48 rows, 4 x 16K             119 / 131;  64 rows 156 / 133
 // (E4M3 rows are converted for the tensor cores first, so they wait longer.)
-static bool use_rows(int fp8, int G, int max_q) { return (long long)max_q * G <= (fp8 ? 128 : 32); }
+static bool use_rows(int fp8, int G, int max_q) { return (long long)max_q * G <= (fp8 ? 128 : 48); }
 
 // In a batch with a long chunk, sequences with one block of rows at most
 // (decoding ones, short drafts) go to the row kernel all the same: a tile of
