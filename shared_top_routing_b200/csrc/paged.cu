@@ -245,8 +245,8 @@ paged_gather_kernel(const uint8_t* __restrict__ kp, const uint8_t* __restrict__ 
 
 constexpr int kRwConsumers = 8;
 // The producer and the three warps beside it (which copy selected rows and are
-// idle otherwise) leave registers to the consumers (8 * 224 + 4 * 56 = 12 * 168; without: 121 us for one token of each of
-// 8 x 32K E4M3 positions, 115 with).
+// idle otherwise) leave registers to the consumers: 8 * 224 + 4 * 56 = 12 * 168
+// (without: 121 us for one token of each of 8 x 32K E4M3 positions, 115 with).
 constexpr int kRwThreads = (kRwConsumers + 4) * 32, kRwConsumerRegs = 224, kRwOtherRegs = 56;
 constexpr int kRwMaxStages = 8;
 // Query rows of a block, in eights: what the consumers' registers hold (drafts
@@ -1179,7 +1179,8 @@ cudaError_t launch_rows(const PagedArgs& a, void* parts, int* err, cudaStream_t 
   const size_t smem = kRwBarBytes + (size_t)pl.stages * 2 * pl.R * pl.row_bytes;
   auto kern = pl.RB <= 8    ? paged_attn_rows_kernel<FP8, SPARSE, 1>
               : pl.RB <= 16 ? paged_attn_rows_kernel<FP8, SPARSE, 2>
-                            : paged_attn_rows_kernel<FP8, SPARSE, FP8 || SPARSE ? 2 : 3>;   // (one token: 16 rows at most)
+                            // (one token: 16 rows at most)
+                            : paged_attn_rows_kernel<FP8, SPARSE, FP8 || SPARSE ? 2 : 3>;
   cudaError_t e = ensure_dynamic_smem((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((unsigned)pl.W), dim3(kRwThreads), smem, st, a, pl, po, pml, err);
