@@ -679,7 +679,7 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
   const size_t stage_bytes = 2 * (size_t)R * rb;
   if (threadIdx.x == 0) {
     for (int s = 0; s < pl.stages; ++s) {
-      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&full[s], SPARSE ? 4 : 1);   // the warps that copy
       tc::mbar_init(&empty[s], kRwConsumers);
     }
     *abort_flag = 0;
@@ -797,7 +797,8 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
         unsigned char* stK = ring + (size_t)s * stage_bytes;
         unsigned char* stV = stK + (size_t)R * rb;
         const int rows = min(R, keys - t * R);   // rows past the last key stay as they are (masked)
-        if (pw == 0 && lane == 0) tc::mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)rows * (uint32_t)rb);
+        const int mine = SPARSE ? (rows + 1 - (pw >> 1)) / 2 : 2 * rows;   // rows this warp copies
+        if (lane == 0) tc::mbar_arrive_expect_tx(&full[s], (uint32_t)mine * (uint32_t)rb);
         __syncwarp();
         if constexpr (SPARSE) {
           int jc[NI], pc[NI];
@@ -840,8 +841,8 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
         ++fill;
       }
     }
-    // every copy this CTA issued lands before it exits
-    for (int s = 0; s < pl.stages && pw == 0; ++s) {
+    // every copy this warp issued lands before the CTA exits
+    for (int s = 0; s < pl.stages; ++s) {
       if ((uint32_t)s < fill) {
         const uint32_t last_use = (fill - 1 - (uint32_t)s) / (uint32_t)pl.stages;
         if (!tc::mbar_wait_drain(&full[s], last_use & 1u) && err) atomicCAS(err, 0, 22);
