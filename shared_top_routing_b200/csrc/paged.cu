@@ -971,6 +971,7 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
     const SeqSpan s = seq_span(a.q_start, a.kv_len, i / pl.nrb, a.N, a.max_pages << a.page_shift);
     const int t0 = i % pl.nrb * pl.tb;
     t = tok - s.begin - t0;
+    if (s.len > a.many) return false;   // the tensor cores' sequence: its tokens have their results
     return t >= 0 && t < pl.tb && t + t0 < min(s.len, a.max_q);
   };
   int p = -1, n_p = 0, t_p = 0;

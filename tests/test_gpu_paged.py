@@ -740,3 +740,52 @@ def test_the_binding_refuses_on_the_gpu():
         sa.sa_paged_kv_write(q, q, *pools, table, qs, kl)
     with pytest.raises(ValueError, match="idx"):
         sa.sa_paged_kv_gather(*pools, table, kl, kl)
+
+
+# ------------------------------------- batches with few tokens for their slots
+
+def _slots_case(kind, slots, G):
+    """q_len of a batch whose packed tokens (two more belong to no sequence)
+    are at most slots * (16 // G), with a chunk of more than 128 rows per kv
+    head, or a bound that allows one."""
+    few = 16 // G
+    room = slots * few - 2
+    if kind == "drafts":          # drafts too long for a block of rows beside single tokens, the bound left out
+        long = max(5, few + 1)
+        n = min(slots // 2, (room - slots) // (long - 1)) if few > 1 else 3
+        ones = slots - n if few > 1 else 8
+        q_len = [long] * n + [1] * ones
+    elif kind == "single tokens":
+        q_len = [128 // G + 8] + [1] * (slots - 1 if few > 1 else 8)
+    else:
+        q_len = [128 // G + 8]
+    q_len += [0] * (slots - len(q_len))
+    q_len = q_len[slots // 3:] + q_len[:slots // 3]
+    assert sum(q_len) <= room and max(q_len) > few
+    return q_len
+
+
+@pytest.mark.parametrize("kv_type", TYPES)
+@pytest.mark.parametrize("hkv", [1, 8])        # rows to fold: fewer than a warp each is used for, or more
+@pytest.mark.parametrize("slots", [28, 40])    # sequences planned by a warp, or by a block
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+@pytest.mark.parametrize("kind", ["single tokens", "idle slots", "drafts"])
+def test_a_long_chunk_in_a_batch_with_few_tokens(kv_type, hkv, slots, G, kind):
+    """A chunk for the tensor cores beside decoding or idle sequences, fewer
+    tokens in all than the blocks of the short ones could hold."""
+    q_len = _slots_case(kind, slots, G)
+    rng = _rng(slots + G)
+    kv = [n + (29 * i) % 150 + 60 * (n > 16 // G) for i, n in enumerate(q_len)]
+    table, num_pages = _table(kv, 16, rng)
+    pools = [_random_pool(G + i, num_pages, 16, hkv, kv_type) for i in range(2)]
+    q_start = np.cumsum([1] + q_len).astype(np.int32)
+    N = int(q_start[-1]) + 1
+    q = _normal(slots, 9, (N, hkv * G, 128))
+    bound = {} if kind == "drafts" else {"max_q": max(q_len)}
+    assert (N if kind == "drafts" else max(q_len)) * G > 128
+    out = torch.full((N, hkv * G, 128), 7.0, dtype=torch.bfloat16, device=dev())
+    _, lse = sa.sa_paged_attn(to_dev(q), *[_dev_pool(p, kv_type) for p in pools], i32(table), i32(q_start), i32(kv),
+                              out=out, with_lse=True, **bound)
+    ref = P.paged_attention(q, *pools, table, q_start, kv, kv_type)
+    _check_attn(out, lse, ref, max(kv))
+    assert (out[0] == 7.0).all() and (out[-1] == 7.0).all()
