@@ -939,6 +939,14 @@ paged_attn_rows_kernel(const PagedArgs a, const RowsPlan pl, float* __restrict__
   }
 }
 
+// A contributor's weight against the reference m.  One that saw nothing (m
+// -inf, l 0, o 0) has none, one whose visible logits are all NaN (m -inf, l NaN)
+// has 1.  No contributor is left out for a weight of 0: 0 times a NaN or an
+// infinity is NaN, as it is in the products of one contributor.
+__device__ __forceinline__ float merge_weight(float2 ml, float m) {
+  return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - m);
+}
+
 // out = sum_x w_x o_x / L, w_x = 2^(m_x - M), L = sum_x w_x l_x, M = max_x m_x
 // over the contributors x of a row's block.  MANY: one CTA per token and 8
 // query heads, a warp each; otherwise one CTA per row.
@@ -1043,15 +1051,13 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
       const float2 ml = lane < nx ? __ldcg(reinterpret_cast<const float2*>(pml + (x0 + lane) * xstride * 2))
                                   : make_float2(-INFINITY, 0.f);
       const float m = fmaxf(M, warp_max(ml.x));
-      // (a NaN sum counts: it belongs in the result)
-      const float w = ml.x != -INFINITY || ml.y != 0.f ? exp2f(ml.x - m) : 0.f;
-      const float f = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : exp2f(M - m);
+      const float w = merge_weight(ml, m);
+      const float f = merge_weight(make_float2(M, L), m);
       M = m;
-      L = (f != 0.f ? L * f : 0.f) + warp_sum(w != 0.f ? ml.y * w : 0.f);
-      acc = f != 0.f ? make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+      L = L * f + warp_sum(ml.y * w);
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
       auto fold = [&](float4 ov, int i) {
         const float wt = __shfl_sync(0xffffffffu, w, i);
-        if (wt == 0.f) return;
         acc.x = fmaf(ov.x, wt, acc.x);
         acc.y = fmaf(ov.y, wt, acc.y);
         acc.z = fmaf(ov.z, wt, acc.z);
@@ -1097,19 +1103,17 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
   float M = rmax[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) M = fmaxf(M, rmax[w]);
-  // (a NaN sum counts: it belongs in the result)
-  auto weight = [&](float2 ml) { return ml.x != -INFINITY || ml.y != 0.f ? exp2f(ml.x - M) : 0.f; };
   float lloc = 0.f;
   if (tid < C) {
-    const float wv = weight(ml0);
+    const float wv = merge_weight(ml0, M);
     wts[tid] = wv;
-    lloc = wv != 0.f ? ml0.y * wv : 0.f;
+    lloc = ml0.y * wv;
   }
   for (int x = tid + kRwMergeThreads; x < C; x += kRwMergeThreads) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(pml + (long long)x * xstride * 2));
-    const float wv = weight(ml);
+    const float wv = merge_weight(ml, M);
     wts[x] = wv;
-    lloc += wv != 0.f ? ml.y * wv : 0.f;
+    lloc += ml.y * wv;
   }
   lloc = warp_sum(lloc);
   if (lane == 0) rsum[warp] = lloc;
@@ -1119,7 +1123,6 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
   for (int w = 0; w < kWarps; ++w) L += rsum[w];
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   auto fold = [&](float4 ov, float wt) {
-    if (wt == 0.f) return;
     acc.x = fmaf(ov.x, wt, acc.x);
     acc.y = fmaf(ov.y, wt, acc.y);
     acc.z = fmaf(ov.z, wt, acc.z);

@@ -789,3 +789,93 @@ def test_a_long_chunk_in_a_batch_with_few_tokens(kv_type, hkv, slots, G, kind):
     ref = P.paged_attention(q, *pools, table, q_start, kv, kv_type)
     _check_attn(out, lse, ref, max(kv))
     assert (out[0] == 7.0).all() and (out[-1] == 7.0).all()
+
+
+# ------------------------------------------------ what the joins have to keep
+
+@pytest.mark.parametrize("kv_type,kv", [(P.BF16, 97), (P.BF16, 129), (P.E4M3, 33), (P.E4M3, 257)])
+@pytest.mark.parametrize("B", [3, 64])         # rows to fold: a block each, or a warp
+@pytest.mark.parametrize("sparse", [False, True])
+def test_a_bad_key_alone_in_its_part_makes_nan(kv_type, kv, B, sparse):
+    """The last key, which no other shares a warp's slice (97, 33) or a tile
+    (129, 257) with, is NaN: so are the output and the log-sum-exp."""
+    hkv, G, page = 1, 16, 16
+    table, num_pages = _table([kv] * B, page, _rng(kv))
+    pools = [_random_pool(150 + i, num_pages, page, hkv, kv_type) for i in range(2)]
+    row = pools[0][table[1, (kv - 1) // page], (kv - 1) % page]
+    if kv_type == P.BF16:
+        row[:256].view(np.uint16)[3] = 0x7FC0
+    else:
+        row[3] = 0x7F
+    q = _normal(31, 1, (B, G, 128))
+    dp = [_dev_pool(p, kv_type) for p in pools]
+    if sparse:
+        idx, count = np.tile(np.arange(kv, dtype=np.int32), (B, 1)), [kv] * B
+        out, lse = sa.sa_paged_sparse_attn_decode(to_dev(q), *dp, i32(table), i32(idx), i32(count), with_lse=True)
+    else:
+        out, lse = sa.sa_paged_attn(to_dev(q), *dp, i32(table), i32(np.arange(B + 1)), i32([kv] * B), 1, with_lse=True)
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    ref = P.paged_attention(q, *pools, table, np.arange(B + 1), [kv] * B, kv_type)
+    for r in ref:
+        r[1] = np.nan                          # (not compared)
+    _check_attn(out, lse, ref, kv)
+
+
+def _faint_case(kv_type, G, q_len, kv, faint, bad):
+    """One sequence, one kv head, every query row the same vector u; the keys
+    that `faint` names are -40 u, so that their weights are far below fp32's
+    least (2^-600 or so of the others'), and V of position `bad`, one of them,
+    holds NaN in element 5: NaN by the definition."""
+    page = 16
+    u = _normal(32, 1, (1, 1, 128))
+    q = np.tile(u, (q_len, G, 1))
+    table, num_pages = _table([kv], page, _rng(33))
+    pools = [_random_pool(160 + i, num_pages, page, 1, kv_type) for i in range(2)]
+    far = ch.f32_to_bf16_bits((-40 * R.bf16_bits_to_f64(u).reshape(-1)).astype(np.float32)).reshape(1, 128)
+    for j in np.flatnonzero(faint(np.arange(kv))):
+        pools[0][table[0, j // page], j % page] = P.make_row(far, kv_type)
+    row = pools[1][table[0, bad // page], bad % page]
+    if kv_type == P.BF16:
+        row[:256].view(np.uint16)[5] = 0x7FC0
+    else:
+        row[5] = 0x7F
+    args = (to_dev(q), *[_dev_pool(p, kv_type) for p in pools], i32(table))
+    ref = P.paged_attention(q, *pools, table, [0, q_len], [kv], kv_type)
+    return args, ref, faint(np.arange(kv))
+
+
+def _check_faint(out, lse, ref, kv):
+    o, l, mag, zabs = ref
+    assert np.isnan(o[..., 5]).all() and not np.isnan(np.delete(o, 5, -1)).any()
+    assert torch.isnan(out[..., 5]).all(), "a NaN value's weight was taken for nothing"
+    clean = out.clone()
+    clean[..., 5] = 0
+    o[..., 5] = mag[..., 5] = 0
+    _check_attn(clean, lse, (o, l, mag, zabs), kv)
+
+
+@pytest.mark.parametrize("kv_type", TYPES)
+@pytest.mark.parametrize("G,q_len", [(16, 1), (1, 3)])
+@pytest.mark.parametrize("sparse", [False, True])
+def test_a_value_that_is_nan_shows_however_little_its_weight(kv_type, G, q_len, sparse):
+    """All keys of a warp's slice (and of a tile) have weights that are nothing
+    beside the others'."""
+    if sparse and q_len > 1:
+        q_len = 1
+    kv = 900
+    args, ref, _ = _faint_case(kv_type, G, q_len, kv, lambda j: j < 256, 7)
+    if sparse:
+        out, lse = sa.sa_paged_sparse_attn_decode(*args, i32(np.arange(kv)[None]), i32([kv]), with_lse=True)
+    else:
+        out, lse = sa.sa_paged_attn(*args, i32([0, q_len]), i32([kv]), q_len, with_lse=True)
+    _check_faint(out, lse, ref, kv)
+
+
+def test_a_value_that_is_nan_shows_when_a_warp_folds_a_row():
+    """As above with enough rows that a warp folds each."""
+    kv, B, G = 900, 64, 16
+    (q, kp, vp, table), ref, _ = _faint_case(P.BF16, G, 1, kv, lambda j: j < 256, 7)
+    out, lse = sa.sa_paged_attn(q.expand(B, G, 128).contiguous(), kp, vp, table.expand(B, -1).contiguous(),
+                                i32(np.arange(B + 1)), i32([kv] * B), 1, with_lse=True)
+    ref = [np.repeat(r, B, 0) for r in ref]
+    _check_faint(out, lse, ref, kv)
