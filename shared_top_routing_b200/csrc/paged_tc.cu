@@ -465,15 +465,20 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
       }
       continue;
     }
+    // (a half or a piece that saw a key counts whatever its weight: 0 times a
+    // NaN or an infinity is NaN, as it is within one product)
+    const bool sawA = cnt > 0 && (m != -INFINITY || l != 0.f);
+    bool sawB = false;
     float fA = 1.f, fB = 0.f;
     const float* other = scratch + (size_t)row * kPgD;
     if (join) {
       named_sync(1, 256);
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(scratch + kTile * kPgD + row * 2));
       const float mb = ml.x, M = fmaxf(m, mb);
+      sawB = mb != -INFINITY || ml.y != 0.f;
       fA = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);
       fB = mb == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(mb - M);
-      l = (fA != 0.f ? l * fA : 0.f) + (fB != 0.f ? ml.y * fB : 0.f);
+      l = l * fA + ml.y * fB;
       m = M;
     }
     const int tok = it.tok0 + t, head = (pl.h0 + it.kvh) * a.G + row % a.G;
@@ -488,7 +493,6 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
       fA *= inv;
       fB *= inv;
     }
-    const bool dead = fA == 0.f || cnt == 0;   // nothing seen: what O holds does not count
     if (any) {
       // (the item's first row of this warp is the base: rows of a warp lie
       // within 32-bit distances of 64-byte units)
@@ -500,8 +504,8 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
         tmem_ld_wait32(o);
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-          o[e] = __float_as_uint(!ok ? __uint_as_float(0x7fc00000u) : dead ? 0.f : __uint_as_float(o[e]) * fA);
-        if (join && fB != 0.f) {
+          o[e] = __float_as_uint(!ok ? __uint_as_float(0x7fc00000u) : sawA ? __uint_as_float(o[e]) * fA : 0.f);
+        if (sawB) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 v = __ldcg(reinterpret_cast<const float4*>(other + 32 * q) + e);
@@ -1049,8 +1053,9 @@ paged_tc_merge_kernel(const PagedArgs a, const TcPlan pl, const TcPiece* __restr
       const float f = M[q] == -INFINITY ? (L[q] == 0.f ? 0.f : 1.f) : exp2f(M[q] - m);
       const float w = ml[q].x == -INFINITY ? 1.f : exp2f(ml[q].x - m);
       M[q] = m;
-      L[q] = (f != 0.f ? L[q] * f : 0.f) + (w != 0.f ? ml[q].y * w : 0.f);
-      auto fold = [&](float acc, float x) { return (f != 0.f ? acc * f : 0.f) + (w != 0.f ? x * w : 0.f); };
+      // (a weight of 0 leaves nothing out: 0 times a NaN is NaN)
+      L[q] = L[q] * f + ml[q].y * w;
+      auto fold = [&](float acc, float x) { return acc * f + x * w; };
       o[q].x = fold(o[q].x, v[q].x);
       o[q].y = fold(o[q].y, v[q].y);
       o[q].z = fold(o[q].z, v[q].z);

@@ -879,3 +879,16 @@ def test_a_value_that_is_nan_shows_when_a_warp_folds_a_row():
                                 i32(np.arange(B + 1)), i32([kv] * B), 1, with_lse=True)
     ref = [np.repeat(r, B, 0) for r in ref]
     _check_faint(out, lse, ref, kv)
+
+
+@pytest.mark.parametrize("kv_type", TYPES)
+@pytest.mark.parametrize("q_len,kv,faint", [
+    (290, 900, lambda j: j < 128),                    # pieces of an item folded by the merge
+    (290, 420, lambda j: j // 128 % 2 == 0),          # a block's even key tiles beside its odd ones
+])
+def test_a_value_that_is_nan_shows_in_a_chunk(kv_type, q_len, kv, faint):
+    """The weights of one part of a row's keys are nothing beside those of the
+    part it is joined with; NaN in that part's values stays."""
+    args, ref, _ = _faint_case(kv_type, 1, q_len, kv, faint, 7)
+    out, lse = sa.sa_paged_attn(*args, i32([0, q_len]), i32([kv]), q_len, with_lse=True)
+    _check_faint(out, lse, ref, kv)
