@@ -528,6 +528,7 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
         }
       }
     }
+    __syncwarp();   // a row is written by four lanes of the warp, and read again below by its own
     if (rowok) {
       if (!direct)
         *reinterpret_cast<float2*>(part_ml + (slot * 2 * kTile + prow) * 2) = make_float2(m, l);

@@ -892,3 +892,33 @@ def test_a_value_that_is_nan_shows_in_a_chunk(kv_type, q_len, kv, faint):
     args, ref, _ = _faint_case(kv_type, 1, q_len, kv, faint, 7)
     out, lse = sa.sa_paged_attn(*args, i32([0, q_len]), i32([kv]), q_len, with_lse=True)
     _check_faint(out, lse, ref, kv)
+
+
+@pytest.mark.parametrize("kv_type", TYPES)
+@pytest.mark.parametrize("q_len,kv", [([300], [400]), ([300], [1500]), ([200, 140], [230, 900])])
+def test_values_that_are_not_finite_all_over_a_chunk(kv_type, q_len, kv):
+    """Every new position has an element of V that is infinite or NaN, another
+    one each: a token shows those of the positions it sees, in rows finished at
+    once and in rows folded from pieces, and the same bits every time."""
+    page, hkv, G = 16, 2, 2
+    table, _ = _table(kv, page, _rng(35))
+
+    def pools(n):
+        out = [_random_pool(170 + i, n, page, hkv, kv_type) for i in range(2)]
+        for b, (T, S) in enumerate(zip(q_len, kv)):
+            for j in range(S - T, S):
+                row, d = out[1][table[b, j // page], j % page], (7 * j) % 256
+                if kv_type == P.BF16:
+                    row[:hkv * 256].view(np.uint16)[d] = 0x7F80
+                else:
+                    row[d] = 0x7F
+        return out
+
+    runs = [_attn_case(35, kv_type, hkv, G, page, q_len, kv, pools=pools) for _ in range(4)]
+    (got, lse, ref, n), bits = runs[0], [bits_of(r[0]) for r in runs]
+    assert all(np.array_equal(b, bits[0]) for b in bits)
+    odd = ~np.isfinite(ref[0])
+    g = got.float().cpu().numpy()
+    assert np.array_equal(~np.isfinite(g), odd)
+    o, mag = (np.where(odd, 0.0, x) for x in (ref[0], ref[2]))
+    _check_attn(torch.from_numpy(np.where(odd, 0.0, g)).to(dev()), lse, (o, ref[1], mag, ref[3]), n)
