@@ -922,3 +922,40 @@ def test_values_that_are_not_finite_all_over_a_chunk(kv_type, q_len, kv):
     assert np.array_equal(~np.isfinite(g), odd)
     o, mag = (np.where(odd, 0.0, x) for x in (ref[0], ref[2]))
     _check_attn(torch.from_numpy(np.where(odd, 0.0, g)).to(dev()), lse, (o, ref[1], mag, ref[3]), n)
+
+
+@pytest.mark.parametrize("kv_type", TYPES)
+def test_host_threads_on_one_stream(kv_type):
+    """Four threads call at once on the default stream, short and long chunks
+    and selected rows, and share its workspace: each gets what it gets alone."""
+    import threading
+
+    hkv, G, page, kv = 2, 4, 16, [1900, 333, 60]
+    table, num_pages = _table(kv, page, _rng(36))
+    pools = [_dev_pool(_random_pool(180 + i, num_pages, page, hkv, kv_type), kv_type) for i in range(2)]
+    tab, lens, work = i32(table), i32(kv), []
+    for i, q_len in enumerate(([1, 1, 1], [90, 3, 1], [4, 40, 2])):
+        q, start = to_dev(_normal(37 + i, 1, (sum(q_len), hkv * G, 128))), i32(np.cumsum([0] + q_len))
+        work.append(lambda q=q, start=start, m=max(q_len): sa.sa_paged_attn(q, *pools, tab, start, lens, m, with_lse=True))
+    qs, idx, cnt = to_dev(_normal(40, 1, (3, hkv * G, 128))), i32(np.tile(np.arange(50), (3, 1))), i32([50, 50, 7])
+    work.append(lambda: sa.sa_paged_sparse_attn_decode(qs, *pools, tab, idx, cnt, with_lse=True))
+    want = [w() for w in work]
+    got, errors, gate = [[] for _ in work], [], threading.Barrier(len(work))
+
+    def run(i):
+        try:
+            gate.wait()
+            for _ in range(60):
+                got[i].append(work[i]())
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for res, (o, l) in zip(got, want):
+        assert len(res) == 60 and all(torch.equal(a, o) and torch.equal(b, l) for a, b in res)

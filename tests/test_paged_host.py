@@ -214,3 +214,73 @@ def test_the_binding_refuses_what_it_cannot_pass_on():
         S._ints32(torch.zeros(2, dtype=torch.int32), "kv_len", dev, (3,))
     with pytest.raises(ValueError, match="out"):
         S._result(torch.zeros(2), "out", dev, (2,), torch.bfloat16)
+
+
+def test_two_threads_on_one_stream_take_the_shared_workspace_in_turn(monkeypatch):
+    """A call's kernels hand results to one another through the stream's
+    workspace: no other thread's call is enqueued between them, and the buffer
+    is not replaced under one."""
+    import threading
+    import time
+
+    S._names()
+    seen = {"inside": 0, "most": 0, "calls": 0, "replaced": 0}
+    alive = {}
+
+    class Torch:
+        @staticmethod
+        def zeros(n, dtype, device):
+            t = torch.zeros(n, dtype=dtype)
+            seen["replaced"] += seen["inside"]
+            alive[t.data_ptr()] = n
+            return t
+
+    class Cuda:
+        @staticmethod
+        def _cuda_isCurrentStreamCapturing():
+            return False
+
+    class Lib:
+        _handle = 0
+
+        @staticmethod
+        def sa_paged_attn_workspace(B, N, max_q, *_):
+            return 256 * max_q
+
+        @staticmethod
+        def sa_paged_attn(*args):
+            ws, nbytes = args[-3], args[-2]
+            assert alive[ws] >= nbytes
+            seen["inside"] += 1
+            seen["most"] = max(seen["most"], seen["inside"])
+            time.sleep(2e-3)          # (between the launches of two kernels)
+            seen["inside"] -= 1
+            seen["calls"] += 1
+            return S.SA_OK
+
+    monkeypatch.setattr(S, "_torch", lambda: Torch)
+    monkeypatch.setattr(S, "_cuda", Cuda)
+    monkeypatch.setattr(S, "_lib", Lib)
+    monkeypatch.setattr(S, "_paged_ws", {})
+    monkeypatch.setattr(S, "_paged_ws_need", {})
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    ints = torch.zeros(4, dtype=torch.int32)
+    pool = torch.zeros(4, 16, 264, dtype=torch.bfloat16)
+    errors = []
+
+    def work(t):
+        try:
+            out = torch.empty_like(q)
+            for i in range(12):
+                S._attn(q, pool, pool, ints, ints, ints, 1 + i + t, 0.0, out, False, None, -1, q.shape, 1024, S.SA_KV_BF16,
+                        2, 4, 16, 2, 2, 77)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    assert seen["calls"] == 48 and seen["most"] == 1 and seen["replaced"] == 0
