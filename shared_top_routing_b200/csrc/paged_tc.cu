@@ -643,11 +643,10 @@ __device__ __forceinline__ void mma_role(const PagedArgs& a, const TcPlan& pl, T
     }
     seq0 += (uint32_t)(it.j1 - it.j0);
   }
-  // (after an abort) everything issued is done before TMEM is freed
-  if (!ok || *abort_flag) {
-    umma_commit(&bars.drain);
-    if (!mbar_wait_drain(&bars.drain, 0) && err) atomicCAS(err, 0, 41);
-  }
+  // everything issued is done before TMEM is freed (an abort by another warp
+  // may still come after this one's last look at the flag)
+  umma_commit(&bars.drain);
+  if (!mbar_wait_drain(&bars.drain, 0) && err) atomicCAS(err, 0, 41);
 }
 
 // ------------------------------------------------------------------- kernel
@@ -855,13 +854,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           }
         }
       }
-      if (!ok || *abort_flag) {   // after an abort: copies in flight land before the CTA exits
+      // every copy issued lands before the CTA exits, whoever gives up later
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-          for (uint32_t i = issued[kv] > kStages ? issued[kv] - kStages : 0; i < issued[kv]; ++i)
-            if (!mbar_wait_drain(kv ? &bars.v_full[i % kStages] : &bars.k_full[i % kStages], (i / kStages) & 1u) && err)
-              atomicCAS(err, 0, 44);
-      }
+      for (int kv = 0; kv < 2; ++kv)
+        for (uint32_t i = issued[kv] > kStages ? issued[kv] - kStages : 0; i < issued[kv]; ++i)
+          if (!mbar_wait_drain(kv ? &bars.v_full[i % kStages] : &bars.k_full[i % kStages], (i / kStages) & 1u) && err)
+            atomicCAS(err, 0, 44);
     } else if (warp == 9) {
       if (elect_lane()) mma_role(a, pl, c, bars, abort_flag, err, smem_u32(sQ), smem_u32(sK), smem_u32(sV), tmem);
       __syncwarp();
@@ -888,9 +886,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                           (pl.h0 + it.kvh) * a.G, it.tok0 + (it.split ? 0 : x * pl.tpt));
           }
         }
-        if (!ok || *abort_flag)
-          for (int x = 0; x < 2; ++x)
-            if (nq[x] > 0 && !mbar_wait_drain(&bars.q_full[x], (nq[x] - 1) & 1u) && err) atomicCAS(err, 0, 45);
+        for (int x = 0; x < 2; ++x)   // (as for K and V)
+          if (nq[x] > 0 && !mbar_wait_drain(&bars.q_full[x], (nq[x] - 1) & 1u) && err) atomicCAS(err, 0, 45);
       }
       __syncwarp();
     }
