@@ -1054,7 +1054,7 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
       const float w = merge_weight(ml, m);
       const float f = merge_weight(make_float2(M, L), m);
       M = m;
-      L = L * f + warp_sum(ml.y * w);
+      L = weighted_sum(L, f, warp_sum(__fmul_rn(ml.y, w)), 1.f);
       acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
       auto fold = [&](float4 ov, int i) {
         const float wt = __shfl_sync(0xffffffffu, w, i);
@@ -1113,7 +1113,7 @@ paged_attn_rows_merge_kernel(const PagedArgs a, const RowsPlan pl, const float* 
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(pml + (long long)x * xstride * 2));
     const float wv = merge_weight(ml, M);
     wts[x] = wv;
-    lloc += ml.y * wv;
+    lloc = weighted_sum(lloc, 1.f, ml.y, wv);
   }
   lloc = warp_sum(lloc);
   if (lane == 0) rsum[warp] = lloc;

@@ -105,6 +105,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// a f + b w, both products rounded before the sum: the same bits whichever
+// part comes first.
+__device__ __forceinline__ float weighted_sum(float a, float f, float b, float w) {
+  return __fadd_rn(__fmul_rn(a, f), __fmul_rn(b, w));
+}
+
 // Eight E4M3 codes times `s` -> eight bf16 values.
 __device__ __forceinline__ uint4 e4m3x8_to_bf16x8(uint2 c, float s) {
   uint32_t r[4];

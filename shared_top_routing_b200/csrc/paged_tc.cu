@@ -478,7 +478,7 @@ __device__ __forceinline__ void softmax_role(const int x, const PagedArgs& a, co
       sawB = mb != -INFINITY || ml.y != 0.f;
       fA = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);
       fB = mb == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(mb - M);
-      l = l * fA + ml.y * fB;
+      l = weighted_sum(l, fA, ml.y, fB);
       m = M;
     }
     const int tok = it.tok0 + t, head = (pl.h0 + it.kvh) * a.G + row % a.G;
@@ -1052,8 +1052,8 @@ paged_tc_merge_kernel(const PagedArgs a, const TcPlan pl, const TcPiece* __restr
       const float w = ml[q].x == -INFINITY ? 1.f : exp2f(ml[q].x - m);
       M[q] = m;
       // (a weight of 0 leaves nothing out: 0 times a NaN is NaN)
-      L[q] = L[q] * f + ml[q].y * w;
-      auto fold = [&](float acc, float x) { return acc * f + x * w; };
+      L[q] = weighted_sum(L[q], f, ml[q].y, w);
+      auto fold = [&](float acc, float x) { return weighted_sum(acc, f, x, w); };
       o[q].x = fold(o[q].x, v[q].x);
       o[q].y = fold(o[q].y, v[q].y);
       o[q].z = fold(o[q].z, v[q].z);
