@@ -544,6 +544,8 @@ def _paged_call(L, name, sizes, ws, dev, raw, *args):
     if ws is not None:
         if ws.get_device() != dev:
             raise ValueError(f"ws must be on {_name(dev)}")
+        if not ws.is_contiguous():   # (an expanded tensor has less memory than elements)
+            raise ValueError("ws must be contiguous")
         st = fn(*args, ws.data_ptr(), ws.numel() * ws.element_size(), raw)
     elif need == 0:
         st = fn(*args, None, 0, raw)

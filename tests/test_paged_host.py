@@ -284,3 +284,33 @@ def test_two_threads_on_one_stream_take_the_shared_workspace_in_turn(monkeypatch
         t.join()
     assert not errors
     assert seen["calls"] == 48 and seen["most"] == 1 and seen["replaced"] == 0
+
+
+def test_a_workspace_with_less_memory_than_elements_is_refused(monkeypatch):
+    """An expanded tensor's size says nothing of its memory; kernels would write
+    beyond it."""
+    S._names()
+    calls = []
+
+    class Lib:
+        _handle = 1
+        sa_paged_attn_workspace = staticmethod(lambda *a: 4096)
+        sa_paged_attn = staticmethod(lambda *a: calls.append(a[-3:-1]) or S.SA_OK)
+
+    monkeypatch.setattr(S, "_lib", Lib)
+    monkeypatch.setattr(S, "_paged_ws_need", {})
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    ints = torch.zeros(4, dtype=torch.int32)
+    pool = torch.zeros(4, 16, 264, dtype=torch.bfloat16)
+
+    def call(ws):
+        S._attn(q, pool, pool, ints, ints, ints, 1, 0.0, torch.empty_like(q), False, ws, -1, q.shape, 1024, S.SA_KV_BF16, 2,
+                4, 16, 2, 2, 77)
+
+    good = torch.zeros(4096, dtype=torch.uint8)
+    call(good)
+    assert calls == [(good.data_ptr(), 4096)]
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(8192, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="ws must be contiguous"):
+            call(ws)
+    assert len(calls) == 1
