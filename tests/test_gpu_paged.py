@@ -959,3 +959,31 @@ def test_host_threads_on_one_stream(kv_type):
     assert not errors
     for res, (o, l) in zip(got, want):
         assert len(res) == 60 and all(torch.equal(a, o) and torch.equal(b, l) for a, b in res)
+
+
+@pytest.mark.parametrize("kv_type", TYPES)
+def test_pools_past_four_gibibytes(kv_type):
+    """Pages at the far end of pools of more than 2^32 bytes: rows written there
+    are read back, and attended to, as from a small pool."""
+    hkv, G, page = 8, 2, 64
+    num_pages = (2 ** 32 + 2 ** 28) // (page * P.row_bytes(kv_type, hkv))
+    dtype, row = (torch.bfloat16, hkv * 128 + 8) if kv_type == P.BF16 else (torch.uint8, hkv * 128 + 16)
+    big = [torch.empty(num_pages, page, row, dtype=dtype, device=dev()) for _ in range(2)]
+    assert big[0].numel() * big[0].element_size() > 2 ** 32
+    q_len, kv = [200, 1, 3], [300, 129, 70]
+    small_table, n = _table(kv, page, _rng(41))
+    far = np.where(small_table >= 0, num_pages - 1 - small_table, small_table).astype(np.int32)
+    small = sa.sa_paged_kv_alloc(n, page, hkv, kv_type, device=dev())
+    lens, whole = i32(kv), np.cumsum([0] + kv)
+    kn, vn = (to_dev(_normal(42 + i, 1, (sum(kv), hkv, 128))) for i in range(2))
+    q, start = to_dev(_normal(44, 1, (sum(q_len), hkv * G, 128))), i32(np.cumsum([0] + q_len))
+    idx, cnt = i32(np.stack([_rng(45 + b).integers(0, m, 48) for b, m in enumerate(kv)])), i32([48, 48, 20])
+    res = []
+    for pools, table in ((small, i32(small_table)), (big, i32(far))):
+        sa.sa_paged_kv_write(kn, vn, *pools, table, i32(whole), lens)
+        res.append([*sa.sa_paged_kv_gather(*pools, table, idx, cnt),
+                    *sa.sa_paged_attn(q, *pools, table, start, lens, max(q_len), with_lse=True),
+                    *sa.sa_paged_attn(q[-3:], *pools, table, i32([0, 1, 2, 3]), lens, 1, with_lse=True),
+                    *sa.sa_paged_sparse_attn_decode(q[:3], *pools, table, idx, cnt, with_lse=True)])
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
