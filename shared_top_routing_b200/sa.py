@@ -8,6 +8,7 @@ function fails loudly; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -513,53 +514,60 @@ def _call_stream(dev, stream):
     return raw, None if _cuda._cuda_getDevice() == dev else _torch().cuda.device(dev)
 
 
-class _Shared:
-    """A stream's workspace, and the lock that a call holds from its look-up
-    until all its kernels are enqueued: they hand results to one another
-    through it, and another host thread's call on the same stream must come
-    before or after them all (and must not see the buffer replaced)."""
-    __slots__ = ("lock", "buf")
-
-    def __init__(self):
-        self.lock, self.buf = threading.Lock(), None
-
-
 _paged_ws: dict = {}
 _paged_ws_need: dict = {}
 
+# A call's kernels hand results to one another through the stream's workspace,
+# and ctypes lets other host threads run meanwhile: a call on the same stream
+# must come before or after them all, and must not replace the buffer between
+# them.  So a lock per stream (default streams of all devices share one) is
+# held from the look-up until all kernels are enqueued; a call that was given a
+# workspace holds none.
+_paged_locks: dict = {}
+_no_lock = contextlib.nullcontext()
 
-def _paged_call(L, name, sizes, ws, dev, raw, *args):
-    """One call that takes a workspace, on a stream whose device is current.
-    Outside a capture, one buffer per stream is kept and grows.  A capture gets
-    a buffer of its own from the graph's memory, zeroed by the graph, so that
-    graphs share none with each other or with calls outside.  Its size is a
-    function of the call's sizes alone and is looked up once."""
-    key = (L._handle, dev, name, sizes)
+
+def _new_lock(raw):
+    return _paged_locks.setdefault(raw, threading.Lock())
+
+
+def _paged_workspace(nbytes: int, dev: int, raw_stream: int):
+    """A workspace for one call on a stream (whose device is current).  Outside
+    a capture, one buffer per stream is kept and grows.  A capture gets a
+    buffer of its own from the graph's memory, zeroed by the graph, so that
+    graphs share none with each other or with calls outside."""
+    if _cuda._cuda_isCurrentStreamCapturing():
+        buf = _torch().empty(nbytes, dtype=_u8, device=f"cuda:{dev}")
+        buf[:SA_WS_ALIGN].zero_()
+        return buf
+    key = (dev, raw_stream)
+    buf = _paged_ws.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = _torch().zeros(nbytes, dtype=_u8, device=f"cuda:{dev}")
+        _paged_ws[key] = buf
+    return buf
+
+
+def _paged_ws_args(L, size_of, sizes, ws, dev, raw):
+    """(pointer, bytes, tensor) of the call's workspace, the tensor to be held
+    until the launch; its size is a function of the call's sizes alone and is
+    looked up once."""
+    key = (L._handle, dev, size_of, sizes)
     need = _paged_ws_need.get(key)
     if need is None:
         if len(_paged_ws_need) > 4096:   # (a server meets new sizes for ever)
             _paged_ws_need.clear()
-        need = _paged_ws_need[key] = getattr(L, name + "_workspace")(*sizes)
-    fn = getattr(L, name)
-    if ws is not None:
-        if ws.get_device() != dev:
-            raise ValueError(f"ws must be on {_name(dev)}")
-        if not ws.is_contiguous():   # (an expanded tensor has less memory than elements)
-            raise ValueError("ws must be contiguous")
-        st = fn(*args, ws.data_ptr(), ws.numel() * ws.element_size(), raw)
-    elif need == 0:
-        st = fn(*args, None, 0, raw)
-    elif _cuda._cuda_isCurrentStreamCapturing():
-        buf = _torch().empty(need, dtype=_u8, device=f"cuda:{dev}")
-        buf[:SA_WS_ALIGN].zero_()
-        st = fn(*args, buf.data_ptr(), need, raw)
-    else:
-        shared = _paged_ws.get((dev, raw)) or _paged_ws.setdefault((dev, raw), _Shared())
-        with shared.lock:
-            if shared.buf is None or shared.buf.numel() < need:
-                shared.buf = _torch().zeros(need, dtype=_u8, device=f"cuda:{dev}")
-            st = fn(*args, shared.buf.data_ptr(), need, raw)
-    _check(st, name)
+        need = _paged_ws_need[key] = getattr(L, size_of)(*sizes)
+    if ws is None:
+        if need == 0:
+            return None, 0, None
+        ws = _paged_workspace(need, dev, raw)
+        return ws.data_ptr(), need, ws
+    if ws.get_device() != dev:
+        raise ValueError(f"ws must be on {_name(dev)}")
+    if not ws.is_contiguous():   # (an expanded tensor has less memory than elements)
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def sa_paged_kv_write(k_new, v_new, k_pages, v_pages, block_table, q_start, kv_len, stream=None):
@@ -688,10 +696,13 @@ def _attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q, scale, out, 
     N, Hq, D = shape
     max_q = N if max_q is None else max_q
     out, lse = _outputs(q, shape, out, with_lse, dev)
-    _paged_call(L, "sa_paged_attn", (B, N, max_q, cols, page_size, Hq, Hkv, D, kv_type), ws, dev, raw, q.data_ptr(), qs,
-                k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), B,
-                N, max_q, cols, pages, page_size, Hq, Hkv, D, kv_type, scale, out.data_ptr(),
-                None if lse is None else lse.data_ptr())
+    with _no_lock if ws is not None else _paged_locks.get(raw) or _new_lock(raw):
+        wp, wn, ws = _paged_ws_args(L, "sa_paged_attn_workspace", (B, N, max_q, cols, page_size, Hq, Hkv, D, kv_type),
+                                    ws, dev, raw)
+        st = L.sa_paged_attn(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                             q_start.data_ptr(), kv_len.data_ptr(), B, N, max_q, cols, pages, page_size, Hq, Hkv, D,
+                             kv_type, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wn, raw)
+    _check(st, "sa_paged_attn")
     return (out, lse) if with_lse else out
 
 
@@ -723,10 +734,13 @@ def _sparse(q, k_pages, v_pages, block_table, idx, count, scale, out, with_lse, 
     L = lib()
     B, Hq, D = shape
     out, lse = _outputs(q, shape, out, with_lse, dev)
-    _paged_call(L, "sa_paged_sparse_attn_decode", (B, Hq, Hkv, D, k, kv_type), ws, dev, raw, q.data_ptr(),
-                k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), idx.data_ptr(), count.data_ptr(), B, cols,
-                pages, page_size, Hq, Hkv, D, k, kv_type, scale, out.data_ptr(),
-                None if lse is None else lse.data_ptr())
+    with _no_lock if ws is not None else _paged_locks.get(raw) or _new_lock(raw):
+        wp, wn, ws = _paged_ws_args(L, "sa_paged_sparse_attn_decode_workspace", (B, Hq, Hkv, D, k, kv_type), ws, dev, raw)
+        st = L.sa_paged_sparse_attn_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                                           idx.data_ptr(), count.data_ptr(), B, cols, pages, page_size, Hq, Hkv, D, k,
+                                           kv_type, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), wp,
+                                           wn, raw)
+    _check(st, "sa_paged_sparse_attn_decode")
     return (out, lse) if with_lse else out
 
 
