@@ -674,7 +674,15 @@ def sa_paged_attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q: int 
 
     q [N, Hq, 128] bf16, the sequences' tokens packed by q_start [B + 1];
     kv_len [B] counts them; max_q bounds the tokens of one sequence (1 for
-    decode; by default N).  Returns out [N, Hq, 128][, lse [N, Hq] fp32]."""
+    decode).  By default it is N, which is always right but plans a batch of
+    single tokens as long chunks: give the bound where it is known (see sa.h).
+    Returns out [N, Hq, 128][, lse [N, Hq] fp32]; rows of tokens that belong to
+    no sequence are left as they were, in an out of the call's own undefined.
+
+    ws: uint8 device memory, zero-filled before first use, for one call at a
+    time.  Without it a buffer per stream is kept for the life of the process
+    (a call captured into a graph gets its own); for long chunks of E4M3 caches
+    it may reach 1 GiB, so a program that wants that memory back passes ws."""
     dev, shape, qs = _tokens(q, "q")
     kv_type, Hkv = _pools(k_pages, v_pages, dev)
     pages, page_size, _ = k_pages.shape
@@ -709,7 +717,8 @@ def _attn(q, k_pages, v_pages, block_table, q_start, kv_len, max_q, scale, out, 
 def sa_paged_sparse_attn_decode(q, k_pages, v_pages, block_table, idx, count, scale: float = 0.0, out=None,
                                 with_lse: bool = False, ws=None, stream=None):
     """sa_sparse_attn_decode over a paged cache: q [B, Hq, 128]; idx [B, k]
-    positions; count [B].  Returns out [B, Hq, 128][, lse [B, Hq] fp32]."""
+    positions; count [B]; ws as for sa_paged_attn.  Returns out [B, Hq, 128][,
+    lse [B, Hq] fp32]."""
     dev, shape, _ = _tokens(q, "q")
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
