@@ -186,7 +186,8 @@ def workspace(nbytes: int, device, key: str = "", stream=None):
     """A cached, zero-filled device workspace of at least ``nbytes`` (256-byte
     aligned).  The decode-attention workspace must start zero-filled; the
     library returns its ticket region to zero after each call, so the cache
-    can hand the same buffer to later calls of any shape."""
+    can hand the same buffer to later calls of any shape.  Host threads that
+    call on one stream at the same time must pass workspaces of their own."""
     torch = _torch()
     if nbytes <= 0:
         return None
